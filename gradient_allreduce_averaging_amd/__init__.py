@@ -10,6 +10,9 @@ Names follow the C ABI: ``plan_buckets``, ``plan_two_bucket``,
 ``bind_params``, ``flatten``, ``bucket_allreduce_avg``,
 ``sync_allreduce_avg``, ``sync_sgd_update``, ``accumulate``, ``unflatten``;
 ``make_sync`` resolves a synchronisation once for repeated calls.
+``rms_norm``, ``rms_norm_grad``, ``distill_loss`` and ``distill_grad`` are the
+operators at the two ends of a language model's backward pass, over every
+rank's tokens in one call.
 """
 from __future__ import annotations
 
@@ -26,6 +29,8 @@ _ORDERS = {"seq": SEQUENTIAL, "sequential": SEQUENTIAL, "ring": RING,
            SEQUENTIAL: SEQUENTIAL, RING: RING}
 F32 = 0
 BF16 = 1
+I8 = 2
+E4M3 = 3
 _DTYPES = {"f32": F32, "float32": F32, "bf16": BF16, "bfloat16": BF16, F32: F32, BF16: BF16}
 
 REGION_BN_BIAS, REGION_BN_WEIGHT, REGION_FC_BIAS, REGION_FC_WEIGHT, REGION_FIRST, REGION_DEEP = range(6)
@@ -39,6 +44,11 @@ class DDPError(RuntimeError):
         self.status = status
         msg = f"{call} failed: {STATUS.get(status, status)}"
         super().__init__(msg + (f" ({detail})" if detail else ""))
+
+
+class _RowsC(ctypes.Structure):
+    """ddp_rows_t."""
+    _fields_ = [("rank", ctypes.c_void_p), ("stride", ctypes.c_int64)]
 
 
 def _hip_runtimes_mapped():
@@ -66,6 +76,7 @@ def _load():
     c_i64p = ctypes.POINTER(ctypes.c_int64)
     c_i32p = ctypes.POINTER(ctypes.c_int32)
     vp = ctypes.c_void_p
+    rp = ctypes.POINTER(_RowsC)
     sig = {
         "ddp_plan_buckets": ([c_i64p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int,
                               ctypes.POINTER(vp)], ctypes.c_int),
@@ -112,6 +123,22 @@ def _load():
                                        ctypes.c_float, vp], ctypes.c_int),
         "ddp_accumulate": ([ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.c_int32, ctypes.c_int64,
                             ctypes.c_int, vp], ctypes.c_int),
+        "ddp_rms_norm": ([c_i64p, ctypes.c_int32, ctypes.c_int64, rp, rp, ctypes.c_int, vp,
+                          ctypes.c_int, ctypes.c_float, rp, rp, ctypes.c_int, vp, vp],
+                         ctypes.c_int),
+        "ddp_rms_norm_grad": ([c_i64p, ctypes.c_int32, ctypes.c_int64, rp, ctypes.c_int, vp,
+                               ctypes.c_int, ctypes.c_float, rp, ctypes.c_int, rp, rp, vp,
+                               ctypes.c_int, ctypes.c_int32, vp, ctypes.c_int64, vp],
+                              ctypes.c_int),
+        "ddp_rms_norm_grad_workspace": ([c_i64p, ctypes.c_int32, ctypes.c_int64], ctypes.c_int64),
+        "ddp_distill_loss": ([c_i64p, ctypes.c_int32, ctypes.c_int64, rp, ctypes.c_int,
+                              ctypes.c_int32, rp, ctypes.c_int, rp, ctypes.c_int32, vp,
+                              ctypes.c_float, vp, vp, vp, ctypes.c_int64, vp], ctypes.c_int),
+        "ddp_distill_grad": ([c_i64p, ctypes.c_int32, ctypes.c_int64, rp, ctypes.c_int,
+                              ctypes.c_int32, rp, ctypes.c_int, rp, ctypes.c_int32, vp,
+                              ctypes.c_float, ctypes.c_float, rp, vp, vp, vp, ctypes.c_int64, vp],
+                             ctypes.c_int),
+        "ddp_distill_workspace": ([c_i64p, ctypes.c_int32, ctypes.c_int64], ctypes.c_int64),
         "ddp_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "ddp_abi_version": ([], ctypes.c_int32),
         "ddp_last_error": ([], ctypes.c_char_p),
@@ -569,6 +596,262 @@ def accumulate(dst: Sequence, src: Sequence, length: Optional[int] = None, strea
     _check(lib.ddp_accumulate(_ptr_array([_dev_ptr(t) for t in dst]),
                               _ptr_array([_dev_ptr(t) for t in src]), len(dst), n, dt,
                               _stream_handle(stream)), "ddp_accumulate")
+
+
+# ---------------------------------------------------------------- rows of tokens
+
+class _Tokens:
+    """The shape of one call's matrices, and every rank's tensors as the C
+    call takes them.  ``like[r]`` is rank r's matrix: [..., width], its rows one
+    fixed distance apart."""
+
+    def __init__(self, like: Sequence, width: Optional[int] = None):
+        import torch
+        self.torch = torch
+        self.device = torch.cuda.current_device()
+        self.n = len(like)
+        if self.n == 0:
+            raise ValueError("no ranks")
+        if like[0].dim() == 0:
+            raise ValueError("a rank's tensor needs a dimension of its own for the width")
+        self.width = like[0].shape[-1] if width is None else int(width)
+        if self.width < 1:
+            raise ValueError("the width is 0")
+        self.rows = [t.numel() // self.width for t in like]
+        self.c_rows = (ctypes.c_int64 * self.n)(*self.rows)
+        self._keep = []
+
+    def check(self, t):
+        """Of this call's device."""
+        if not t.is_cuda:
+            raise ValueError("tensor is not on a GPU")
+        if t.get_device() != self.device:
+            raise ValueError("tensor is not on the current GPU")
+
+    def matrix(self, ts, what: str, dtypes, width: Optional[int] = None):
+        """(dtype, ddp_rows_t) of one operand; None, None where it is absent."""
+        if ts is None:
+            return None, None
+        width = self.width if width is None else width
+        if len(ts) != self.n:
+            raise ValueError(f"{what}: one tensor per rank is required")
+        dtype, stride = ts[0].dtype, None
+        if dtype not in dtypes:
+            raise TypeError(f"{what}: unsupported dtype {dtype}")
+        ptrs = []
+        for t, n in zip(ts, self.rows):
+            self.check(t)
+            if t.dtype != dtype:
+                raise ValueError(f"{what}: the ranks differ in dtype")
+            if t.dim() == 0 or t.shape[-1] != width or t.numel() != n * width:
+                raise ValueError(f"{what}: {n} rows of {width} elements are required, "
+                                 f"got {tuple(t.shape)}")
+            if n > 0 and width > 1 and t.stride(-1) != 1:
+                raise ValueError(f"{what}: the elements of a row are not consecutive")
+            if n > 1:
+                if t.dim() == 2:
+                    st = t.stride(0)
+                else:
+                    try:
+                        st = t.view(-1, width).stride(0)
+                    except RuntimeError:
+                        raise ValueError(f"{what}: the rows are not one fixed distance apart") from None
+                if stride is not None and st != stride:
+                    raise ValueError(f"{what}: the ranks differ in row stride")
+                stride = st
+            ptrs.append(t.data_ptr())
+        arr = (ctypes.c_void_p * self.n)(*ptrs)
+        self._keep.append(arr)
+        return dtype, _RowsC(ctypes.addressof(arr), width if stride is None else stride)
+
+    def vectors(self, ts, what: str, length=None, dtypes=None):
+        """(dtype, pointer array) of one vector per rank: ``length`` elements, or one for
+        each of the rank's rows."""
+        if ts is None:
+            return None, None
+        if len(ts) != self.n:
+            raise ValueError(f"{what}: one tensor per rank is required")
+        dtype = ts[0].dtype
+        if dtype not in (dtypes or (self.torch.float32,)):
+            raise TypeError(f"{what}: unsupported dtype {dtype}")
+        for t, n in zip(ts, self.rows):
+            self.check(t)
+            if t.dtype != dtype:
+                raise ValueError(f"{what}: the ranks differ in dtype")
+            if t.numel() != (n if length is None else length):
+                raise ValueError(f"{what}: {n if length is None else length} elements are required, "
+                                 f"got {t.numel()}")
+            if not t.is_contiguous():
+                raise ValueError(f"{what}: tensor is not contiguous")
+        return dtype, (ctypes.c_void_p * self.n)(*[t.data_ptr() for t in ts])
+
+    def shared(self, t, what: str, length: int):
+        """Address of a tensor every rank shares."""
+        self.check(t)
+        if t.numel() != length:
+            raise ValueError(f"{what}: {length} elements are required, got {t.numel()}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: tensor is not contiguous")
+        return t.data_ptr()
+
+    def workspace(self, t, need: int, stream):
+        """(address, bytes, tensor) of the caller's workspace, or of a new one that belongs to
+        the call's stream."""
+        if need < 0:
+            raise DDPError(1, "workspace")
+        torch = self.torch
+        if t is None:
+            if stream is None:
+                t = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+            else:
+                s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+                with torch.cuda.stream(s):
+                    t = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        else:
+            self.check(t)
+            if not t.is_contiguous():
+                raise ValueError("workspace: tensor is not contiguous")
+        return t.data_ptr(), t.numel() * t.element_size(), t
+
+
+def _float_codes(torch):
+    return {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def rms_norm(x: Sequence, weight, out: Sequence, residual: Optional[Sequence] = None,
+             sum_out: Optional[Sequence] = None, scale: Optional[Sequence] = None,
+             eps: float = 1e-6, stream=None):
+    """out[r] = s * weight / sqrt(mean(s^2) + eps) over the last dimension, s = x[r] +
+    residual[r], for every rank in one launch (``ddp_rms_norm``).  ``sum_out``
+    receives s; an int8 or float8_e4m3fn ``out`` comes with ``scale``, one f32 per row."""
+    tk = _Tokens(x)
+    torch = tk.torch
+    codes = _float_codes(torch)
+    dt, xr = tk.matrix(x, "x", codes)
+    codes8 = {**codes, torch.int8: I8, torch.float8_e4m3fn: E4M3}
+    ydt, yr = tk.matrix(out, "out", codes8)
+    rdt, rr = tk.matrix(residual, "residual", codes)
+    sdt, sr = tk.matrix(sum_out, "sum_out", codes)
+    if rdt not in (None, dt) or sdt not in (None, dt):
+        raise ValueError("residual and sum_out must have x's dtype")
+    _, sc = tk.vectors(scale, "scale")
+    wp, wdt = None, F32
+    if weight is not None:
+        wp = tk.shared(weight, "weight", tk.width)
+        if weight.dtype not in codes:
+            raise TypeError(f"weight: unsupported dtype {weight.dtype}")
+        wdt = codes[weight.dtype]
+    _check(lib.ddp_rms_norm(tk.c_rows, tk.n, tk.width, xr, rr, codes[dt], wp, wdt, eps, sr, yr,
+                            codes8[ydt], sc, _stream_handle(stream)), "ddp_rms_norm")
+
+
+def _rows_of(rows):
+    rows = [int(n) for n in rows]
+    return (ctypes.c_int64 * len(rows))(*rows), len(rows)
+
+
+def rms_norm_grad_workspace(rows: Sequence[int], width: int) -> int:
+    """Bytes of workspace ``rms_norm_grad`` needs for ranks of ``rows[r]`` rows."""
+    c, n = _rows_of(rows)
+    need = lib.ddp_rms_norm_grad_workspace(c, n, int(width))
+    if need < 0:
+        raise DDPError(1, "ddp_rms_norm_grad_workspace")
+    return need
+
+
+def rms_norm_grad(s: Sequence, weight, dy: Sequence, dx: Sequence, dsum: Optional[Sequence] = None,
+                  dweight: Optional[Sequence] = None, accumulate: bool = False, eps: float = 1e-6,
+                  workspace=None, stream=None):
+    """The backward of ``rms_norm`` (``ddp_rms_norm_grad``): dx[r] the gradient of
+    s[r] (so of x and the residual), dweight[r] the rank's weight gradient, stored or, with
+    ``accumulate``, added to what is there."""
+    tk = _Tokens(s)
+    torch = tk.torch
+    codes = _float_codes(torch)
+    dt, sr = tk.matrix(s, "s", codes)
+    ydt, yr = tk.matrix(dy, "dy", codes)
+    ddt, dr = tk.matrix(dsum, "dsum", codes)
+    xdt, xr = tk.matrix(dx, "dx", codes)
+    if xdt != dt or ddt not in (None, dt):
+        raise ValueError("dx and dsum must have s's dtype")
+    wp, wdt = None, F32
+    if weight is not None:
+        wp = tk.shared(weight, "weight", tk.width)
+        if weight.dtype not in codes:
+            raise TypeError(f"weight: unsupported dtype {weight.dtype}")
+        wdt = codes[weight.dtype]
+    wgdt, wg = tk.vectors(dweight, "dweight", tk.width, codes)
+    ws, nbytes, keep = None, 0, None
+    if dweight is not None:
+        need = lib.ddp_rms_norm_grad_workspace(tk.c_rows, tk.n, tk.width) if workspace is None else 0
+        ws, nbytes, keep = tk.workspace(workspace, need, stream)
+    _check(lib.ddp_rms_norm_grad(tk.c_rows, tk.n, tk.width, sr, codes[dt], wp, wdt, eps, yr,
+                                 codes[ydt], dr, xr, wg, codes.get(wgdt, F32),
+                                 1 if accumulate else 0, ws, nbytes, _stream_handle(stream)),
+           "ddp_rms_norm_grad")
+
+
+def distill_workspace(rows: Sequence[int], vocab: int) -> int:
+    """Bytes of workspace ``distill_loss`` and ``distill_grad`` need for ranks of
+    ``rows[r]`` tokens."""
+    c, n = _rows_of(rows)
+    need = lib.ddp_distill_workspace(c, n, int(vocab))
+    if need < 0:
+        raise DDPError(1, "ddp_distill_workspace")
+    return need
+
+
+def _distill(logits, teacher, index, dlogits, loss, row_loss, token_weight, temperature, grad_scale,
+             workspace, stream):
+    tk = _Tokens(logits)
+    torch = tk.torch
+    codes = _float_codes(torch)
+    dt, zr = tk.matrix(logits, "logits", codes)
+    if len(teacher) != tk.n or teacher[0].dim() == 0:
+        raise ValueError("teacher: one tensor per rank is required")
+    top = teacher[0].shape[-1]
+    tdt, tr = tk.matrix(teacher, "teacher", codes, top)
+    idt, ir = tk.matrix(index, "index", (torch.int32, torch.int64), top)
+    _, tw = tk.vectors(token_weight, "token_weight")
+    _, rl = tk.vectors(row_loss, "row_loss")
+    lp = tk.shared(loss, "loss", 1)
+    if loss.dtype != torch.float32:
+        raise TypeError(f"loss: unsupported dtype {loss.dtype}")
+    need = lib.ddp_distill_workspace(tk.c_rows, tk.n, tk.width) if workspace is None else 0
+    ws, nbytes, keep = tk.workspace(workspace, need, stream)
+    head = (tk.c_rows, tk.n, tk.width, zr, codes[dt], top, tr, codes[tdt], ir,
+            4 if idt == torch.int32 else 8, tw, temperature)
+    tail = (lp, rl, ws, nbytes, _stream_handle(stream))
+    if dlogits is None:
+        _check(lib.ddp_distill_loss(*head, *tail), "ddp_distill_loss")
+        return
+    gdt, gr = tk.matrix(dlogits, "dlogits", codes)
+    if gdt != dt:
+        raise ValueError("dlogits must have the logits' dtype")
+    _check(lib.ddp_distill_grad(*head, grad_scale, gr, *tail), "ddp_distill_grad")
+
+
+def distill_loss(logits: Sequence, teacher: Sequence, index: Sequence, loss,
+                 row_loss: Optional[Sequence] = None, token_weight: Optional[Sequence] = None,
+                 temperature: float = 1.0, workspace=None, stream=None):
+    """The student's divergence from a teacher known by its top logits
+    (``ddp_distill_loss``): ``teacher[r]`` [..., top] holds them and ``index[r]`` their
+    places in the vocabulary (negative: no entry).  ``loss`` (one f32) receives the weighted
+    mean over the live tokens of all ranks, ``row_loss[r]`` each token's."""
+    _distill(logits, teacher, index, None, loss, row_loss, token_weight, temperature, 1.0, workspace,
+             stream)
+
+
+def distill_grad(logits: Sequence, teacher: Sequence, index: Sequence, dlogits: Sequence, loss,
+                 row_loss: Optional[Sequence] = None, token_weight: Optional[Sequence] = None,
+                 temperature: float = 1.0, grad_scale: float = 1.0, workspace=None, stream=None):
+    """``distill_loss`` and its gradient (``ddp_distill_grad``): what follows from
+    ``dlogits``, averaged over the ranks by a sync, is the gradient of grad_scale * loss.
+    ``dlogits[r]`` may be ``logits[r]``."""
+    if dlogits is None:
+        raise ValueError("dlogits is required")
+    _distill(logits, teacher, index, dlogits, loss, row_loss, token_weight, temperature, grad_scale,
+             workspace, stream)
 
 
 def status_string(status: int) -> str:

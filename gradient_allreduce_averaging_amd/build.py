@@ -13,7 +13,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libddp.so")
 SOURCES = ["plan.cpp", "common.hip", "reduce.hip", "accumulate.hip", "copy.hip", "params.hip",
-           "noalloc.hip"]
+           "noalloc.hip", "rows.cpp", "norm.hip", "distill.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

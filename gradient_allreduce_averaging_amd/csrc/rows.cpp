@@ -1,0 +1,106 @@
+// Host-side checks of the matrices of tokens (declared in rows.h).
+#include "rows.h"
+
+#include <algorithm>
+
+namespace ddp_detail {
+
+namespace {
+
+// No tensor of a call reaches this many bytes, so that no product below
+// overflows.
+constexpr int64_t kMostBytes = int64_t(1) << 60;
+
+// The bytes of one rank's share of an operand: `rows` pieces of `piece` bytes,
+// `pitch` apart.
+struct Extent {
+    uintptr_t lo, hi;
+    int64_t pitch, piece;
+    int64_t rows;
+    int esz;
+    int rank;        // -1: shared by every rank
+    bool written, in_place;
+};
+
+bool same(const Extent &a, const Extent &b)
+{
+    return a.lo == b.lo && a.rows == b.rows && a.piece == b.piece && a.esz == b.esz &&
+           (a.rows == 1 || a.pitch == b.pitch);
+}
+
+// Whether two extents with lo < other's hi share a byte.
+bool meet(const Extent &a, const Extent &b)
+{
+    if (a.hi <= b.lo || b.hi <= a.lo) return false;
+    // rows of one buffer that interleave: every row of b lies in a gap of a
+    if (a.rows > 1 && b.rows > 1 && a.pitch == b.pitch) {
+        const uintptr_t pitch = (uintptr_t)a.pitch;
+        const uintptr_t d = b.lo >= a.lo ? (b.lo - a.lo) % pitch
+                                         : (pitch - (a.lo - b.lo) % pitch) % pitch;
+        if (d >= (uintptr_t)a.piece && d + (uintptr_t)b.piece <= pitch) return false;
+    }
+    return true;
+}
+
+bool allowed(const Extent &a, const Extent &b)
+{
+    if (!a.written && !b.written) return true;
+    if (a.written && b.written) return false;
+    const Extent &in = a.written ? b : a;
+    return in.in_place && a.rank == b.rank && same(a, b);
+}
+
+}  // namespace
+
+ddp_status_t check_shape(const int64_t *rows, int32_t n_ranks, int64_t width, int64_t *total,
+                         int64_t *most)
+{
+    if (!rows || n_ranks < 1 || width < 1) return DDP_ERR_INVALID_ARG;
+    if (n_ranks > DDP_MAX_RANKS) return DDP_ERR_UNSUPPORTED;
+    if (width > kMostBytes / 8) return DDP_ERR_OVERFLOW;
+    *total = *most = 0;
+    for (int r = 0; r < n_ranks; ++r) {
+        if (rows[r] < 0) return DDP_ERR_INVALID_ARG;
+        if (rows[r] > kMostBytes / 8 / width) return DDP_ERR_OVERFLOW;
+        *total += rows[r];   // at most 64 * 2^57
+        *most = std::max(*most, rows[r]);
+    }
+    return DDP_OK;
+}
+
+ddp_status_t check_operands(const Operand *op, int n, int32_t n_ranks)
+{
+    Extent e[kMaxOperands * DDP_MAX_RANKS];
+    int m = 0;
+    for (int k = 0; k < n; ++k) {
+        const Operand &o = op[k];
+        const int shares = o.rank || !o.span ? n_ranks : 1;
+        for (int r = 0; r < shares; ++r) {
+            Extent x;
+            x.rows = o.rows ? o.rows[r] : 1;
+            if (x.rows == 0) continue;
+            if (!o.rank && !o.span) return DDP_ERR_INVALID_ARG;
+            x.lo = reinterpret_cast<uintptr_t>(o.rank ? static_cast<const void *>(o.rank[r]) : o.span);
+            if (!x.lo || x.lo % (uintptr_t)o.esz) return DDP_ERR_INVALID_ARG;
+            if (x.rows > 1 && o.stride < o.width) return DDP_ERR_INVALID_ARG;
+            x.piece = o.width * o.esz;
+            x.pitch = x.rows > 1 ? o.stride : o.width;
+            if (x.pitch > kMostBytes / o.esz / x.rows) return DDP_ERR_OVERFLOW;
+            x.pitch *= o.esz;
+            x.hi = x.lo + (uintptr_t)((x.rows - 1) * x.pitch + x.piece);
+            if (x.hi < x.lo) return DDP_ERR_OVERFLOW;
+            x.esz = o.esz;
+            x.rank = o.rank ? r : -1;
+            x.written = o.written;
+            x.in_place = o.in_place;
+            e[m++] = x;
+        }
+    }
+    std::sort(e, e + m, [](const Extent &a, const Extent &b) { return a.lo < b.lo; });
+    for (int i = 0; i < m; ++i)
+        for (int j = i + 1; j < m && e[j].lo < e[i].hi; ++j)
+            if (!allowed(e[i], e[j]) && meet(e[i], e[j])) return DDP_ERR_ALIAS;
+    return DDP_OK;
+}
+
+}  // namespace ddp_detail

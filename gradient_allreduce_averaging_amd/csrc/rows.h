@@ -1,0 +1,54 @@
+// The matrices of tokens that ddp_rms_norm* and ddp_distill_* take: their
+// host-side checks (rows.cpp).  Not part of the ABI.
+#pragma once
+
+#include <cstdint>
+
+#include "ddp.h"
+
+namespace ddp_detail {
+
+// One operand of a call.  Rows of `width` elements of `esz` bytes, rows[r] of
+// them for rank r, or one span shared by every rank.
+struct Operand {
+    const char *const *rank;   // [n_ranks] addresses, or null for a span
+    const void *span;          // the span's address
+    int64_t stride;            // elements from row to row
+    int64_t width;             // elements of a row, or of the span
+    int esz;                   // bytes per element
+    const int64_t *rows;       // [n_ranks] rows of each rank; null: one row each
+    bool written;
+    bool in_place;             // an input that a written operand may be exactly
+};
+
+inline Operand rows_operand(const ddp_rows_t *m, const int64_t *rows, int64_t width, int esz,
+                            bool written, bool in_place)
+{
+    return {reinterpret_cast<const char *const *>(m->rank), nullptr, m->stride, width, esz, rows,
+            written, in_place};
+}
+// A vector of rows[r] (per_row) or `width` elements for each rank.
+inline Operand vector_operand(const void *const *p, const int64_t *rows, int64_t width, int esz,
+                              bool written)
+{
+    return {reinterpret_cast<const char *const *>(p), nullptr, width, width, esz, rows, written,
+            false};
+}
+inline Operand span_operand(const void *p, int64_t width, int esz, bool written)
+{
+    return {nullptr, p, width, width, esz, nullptr, written, false};
+}
+
+// rows[n_ranks] and the width of a call's matrices: INVALID_ARG, UNSUPPORTED
+// or OVERFLOW where they are refused; *total and *most receive the sum and
+// the largest of the row counts.
+ddp_status_t check_shape(const int64_t *rows, int32_t n_ranks, int64_t width, int64_t *total,
+                         int64_t *most);
+
+// Null or misaligned addresses and short strides (INVALID_ARG), sizes past
+// the int64 layout (OVERFLOW), and written operands that overlap another
+// operand other than in place (ALIAS).  At most kMaxOperands operands.
+constexpr int kMaxOperands = 10;
+ddp_status_t check_operands(const Operand *op, int n, int32_t n_ranks);
+
+}  // namespace ddp_detail

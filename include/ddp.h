@@ -73,10 +73,14 @@ typedef enum {
     DDP_ERR_HIP = 5,           /* a HIP runtime call failed */
     DDP_ERR_NOMEM = 6,         /* host or device allocation failed */
     DDP_ERR_CAPACITY = 7       /* beyond a fixed capacity (the no-allocation
-                                  entry point's static buffer) */
+                                  entry point's static buffer), or a caller's
+                                  workspace that is too small */
 } ddp_status_t;
 
-typedef enum { DDP_F32 = 0, DDP_BF16 = 1 } ddp_dtype_t;
+/* DDP_I8 (two's complement) and DDP_E4M3 (8-bit floats of 4 exponent and 3
+ * mantissa bits, largest 448, no infinities) are outputs of ddp_rms_norm
+ * only: every other call refuses them. */
+typedef enum { DDP_F32 = 0, DDP_BF16 = 1, DDP_I8 = 2, DDP_E4M3 = 3 } ddp_dtype_t;
 
 typedef enum {
     DDP_ORDER_SEQUENTIAL = 0,  /* acc = +0; acc += x_0; ...; acc += x_{N-1} */
@@ -417,6 +421,158 @@ DDP_API void ddp_param_sync_free(ddp_param_sync_t *sync);
  * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW, ALIAS, HIP. */
 DDP_API ddp_status_t ddp_accumulate(void *const *dst, const void *const *src, int32_t n_bufs, int64_t len,
                             ddp_dtype_t dtype, void *stream);
+
+/* ------------------------------------------------- where gradients come from
+ * The two ends of a language model's backward pass, for the N ranks whose
+ * gradients the calls above average: the loss that starts it, and the norm
+ * whose weight gradient lands in a bucket.  Like ddp_accumulate each call
+ * takes every rank's tensors at once.
+ *
+ * A rank's tensor is a matrix of tokens: rows[r] rows (tokens; 0 is allowed,
+ * ranks may differ) of `width` consecutive elements.  rank[r] is the first
+ * element of rank r's first row (not looked at where rows[r] is 0); rows lie
+ * `stride` elements apart, the same for every rank (at least the width,
+ * unless no rank has more than one row).  Any element alignment will do, and
+ * bytes between rows are neither read nor written.
+ * A written tensor may be exactly one of the same rank's row inputs, as named
+ * at each call (same address, stride and element size); it may overlap
+ * nothing else, except that rows of one buffer with the same stride may
+ * interleave (DDP_ERR_ALIAS).  Inputs may overlap each other.
+ * Workspaces belong to the caller, 16-byte aligned, of at least the bytes the
+ * call's own _workspace function gives (DDP_ERR_CAPACITY); what they hold
+ * before and after a call does not matter.  Two calls that may run at the
+ * same time (on two streams, or in two captured graphs) need one each. */
+typedef struct {
+    void *const *rank;         /* host array [n_ranks] of device pointers */
+    int64_t stride;            /* elements from one row to the next */
+} ddp_rows_t;
+
+/* Root-mean-square norm of a residual sum.  For every row:
+ *     s = x + residual                (f32 add, rounded to dtype; s = x without)
+ *     y = s * weight / sqrt(mean(s^2) + eps)           (f32, rounded once)
+ *   rows[n_ranks], n_ranks, width  the matrices' shape; width >= 1
+ *   x, residual    rows of dtype (f32 or bf16); residual NULL for none
+ *   weight         device, `width` elements of weight_dtype (f32 or bf16),
+ *                  the same for every rank, or NULL for ones
+ *   eps            >= 0
+ *   sum_out        rows of dtype that receive s, or NULL; may be exactly x
+ *                  or the residual
+ *   y              rows of y_dtype: dtype, or bf16 for an f32 dtype, or 8 bits
+ *                  (DDP_I8, DDP_E4M3); may be exactly x or the residual where
+ *                  the element sizes match
+ *   scale          host array [n_ranks] of device pointers to rows[r] floats,
+ *                  for an 8-bit y: with most = max |y| of the row and top =
+ *                  127 (I8) or 448 (E4M3), scale = most / top and the codes
+ *                  are y * (top / most) to the nearest, ties to even, so that
+ *                  code * scale stands for y.  A row of zeros has scale 0 and
+ *                  codes 0; a row with a NaN has a NaN scale and codes of no
+ *                  meaning.  NULL for other y_dtype
+ * Squares are summed in f32: a row whose sum of s^2 passes 3.4e38 comes out
+ * as zeros (NaN where s is infinite).  A row with a NaN comes out as NaN.
+ * One launch.  No work where no rank has a row.
+ * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW, ALIAS, HIP. */
+DDP_API ddp_status_t ddp_rms_norm(const int64_t *rows, int32_t n_ranks, int64_t width,
+                                  const ddp_rows_t *x, const ddp_rows_t *residual,
+                                  ddp_dtype_t dtype, const void *weight, ddp_dtype_t weight_dtype,
+                                  float eps, const ddp_rows_t *sum_out, const ddp_rows_t *y,
+                                  ddp_dtype_t y_dtype, float *const *scale, void *stream);
+
+/* Its backward.  With rho = 1 / sqrt(mean(s^2) + eps) of the row and
+ * g = weight * dy:
+ *     dx          = dsum + rho * (g - s * rho^2 * mean(g * s))
+ *     dweight_r   = sum over rank r's rows of dy * s * rho
+ *   s           rows of dtype: the sum the forward call normed (its sum_out,
+ *               or x where there was no residual)
+ *   dy          rows of dy_dtype (dtype, or bf16 for an f32 dtype): the
+ *               gradient of y (of the value code * scale stands for, where y
+ *               was held in 8 bits)
+ *   dsum        rows of dtype: what reaches s past the norm (the gradient of
+ *               sum_out), or NULL for none
+ *   dx          rows of dtype: the gradient of s, which is that of x and of
+ *               the residual alike; may be exactly s, dy or dsum where the
+ *               element sizes match
+ *   dweight     host array [n_ranks] of device pointers to `width` elements
+ *               of dweight_dtype (f32 or bf16), e.g. the weight's place in
+ *               each rank's flat gradient; NULL for none.  accumulate == 0
+ *               stores the sum (rounded once); otherwise the sum is added to
+ *               what is there, f32 add, one rounding (a no_sync micro-step, as
+ *               ddp_accumulate)
+ *   workspace   ddp_rms_norm_grad_workspace(rows, n_ranks, width) bytes; not
+ *               looked at without dweight
+ * Sums are taken in f32 in an order that depends on the shape alone: the same
+ * inputs give the same bits.  A rank without rows has a dweight of zeros.
+ * Two launches (one without dweight).
+ * Errors: as ddp_rms_norm, plus CAPACITY. */
+DDP_API ddp_status_t ddp_rms_norm_grad(const int64_t *rows, int32_t n_ranks, int64_t width,
+                                       const ddp_rows_t *s, ddp_dtype_t dtype, const void *weight,
+                                       ddp_dtype_t weight_dtype, float eps, const ddp_rows_t *dy,
+                                       ddp_dtype_t dy_dtype, const ddp_rows_t *dsum,
+                                       const ddp_rows_t *dx, void *const *dweight,
+                                       ddp_dtype_t dweight_dtype, int32_t accumulate,
+                                       void *workspace, int64_t workspace_bytes, void *stream);
+/* Bytes of workspace, or -1 for arguments the call would refuse. */
+DDP_API int64_t ddp_rms_norm_grad_workspace(const int64_t *rows, int32_t n_ranks, int64_t width);
+
+/* Most teacher entries a token may have. */
+#define DDP_MAX_TOP 1024
+
+/* Distillation: the divergence of a student's distribution over `vocab` from
+ * a teacher known by its `top` largest logits of each token.
+ *   an entry is live      when 0 <= index < vocab and its logit > -infinity;
+ *                         what any other entry holds is not looked at
+ *   a token is live       when it has a live entry and its weight is > 0
+ *   p = softmax(teacher / temperature) over the token's live entries
+ *   q = softmax(logits / temperature) over the vocabulary
+ *     row_loss = temperature^2 * sum over live entries of p (log p - log q)
+ *     loss     = sum of weight * row_loss / D over the live tokens of ALL
+ *                ranks, D = the sum of their weights; 0 if there is none
+ * The logits of a token that is not live are not looked at; its row_loss is 0.
+ * An index named by several entries has the sum of their p.
+ *   logits        rows of `vocab` elements of dtype (f32 or bf16); vocab >= 1.
+ *                 A logit of -infinity has q = 0.  A live token with a NaN, with
+ *                 +infinity or with nothing but -infinity has a NaN loss
+ *   top           teacher entries of a token, 1..DDP_MAX_TOP
+ *   teacher       rows of `top` elements of teacher_dtype (f32 or bf16)
+ *   index         rows of `top` vocabulary indices of index_bytes (4 or 8)
+ *                 bytes, signed; out of [0, vocab): no entry
+ *   token_weight  host array [n_ranks] of device pointers to rows[r] floats,
+ *                 or NULL for ones.  A weight that is not > 0 (NaN included)
+ *                 masks its token
+ *   temperature   > 0
+ *   loss          device, one float
+ *   row_loss      host array [n_ranks] of device pointers to rows[r] floats, or
+ *                 NULL
+ *   workspace     ddp_distill_workspace(rows, n_ranks, vocab) bytes
+ * Sums are taken in f32 in an order that depends on the shape alone.
+ * Errors: INVALID_ARG, UNSUPPORTED (top or rank count beyond the library's),
+ * OVERFLOW, ALIAS, CAPACITY, HIP. */
+DDP_API ddp_status_t ddp_distill_loss(const int64_t *rows, int32_t n_ranks, int64_t vocab,
+                                      const ddp_rows_t *logits, ddp_dtype_t dtype, int32_t top,
+                                      const ddp_rows_t *teacher, ddp_dtype_t teacher_dtype,
+                                      const ddp_rows_t *index, int32_t index_bytes,
+                                      const float *const *token_weight, float temperature,
+                                      float *loss, float *const *row_loss, void *workspace,
+                                      int64_t workspace_bytes, void *stream);
+
+/* The loss and its gradient in one pass over the logits:
+ *     dlogits_j = grad_scale * n_ranks * (weight / D) * temperature * (q_j - p_j)
+ * rounded once to dtype, zeros for a token that is not live.  n_ranks is there
+ * because the synchronisation scales by 1 / n_ranks: the gradients that follow
+ * from these, averaged over the ranks, are those of grad_scale * loss, however
+ * unevenly the live tokens are spread (the average of per-rank means is not).
+ *   grad_scale    e.g. 1 / micro-steps, or a loss scale
+ *   dlogits       rows of `vocab` elements of dtype; may be exactly logits
+ * Errors: as ddp_distill_loss. */
+DDP_API ddp_status_t ddp_distill_grad(const int64_t *rows, int32_t n_ranks, int64_t vocab,
+                                      const ddp_rows_t *logits, ddp_dtype_t dtype, int32_t top,
+                                      const ddp_rows_t *teacher, ddp_dtype_t teacher_dtype,
+                                      const ddp_rows_t *index, int32_t index_bytes,
+                                      const float *const *token_weight, float temperature,
+                                      float grad_scale, const ddp_rows_t *dlogits, float *loss,
+                                      float *const *row_loss, void *workspace,
+                                      int64_t workspace_bytes, void *stream);
+/* Bytes of workspace of either call, or -1 for arguments they would refuse. */
+DDP_API int64_t ddp_distill_workspace(const int64_t *rows, int32_t n_ranks, int64_t vocab);
 
 /* ------------------------------------------------------------ no allocation
  * For callers that cannot allocate device memory: code under HIP graph

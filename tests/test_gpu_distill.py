@@ -1,0 +1,349 @@
+"""ddp_distill_loss and ddp_distill_grad on the GPU against their definition in
+64 bits (bounds derived in rows_util.py): vocabularies from 1 past every
+vector and block, one token to many, ragged ranks, masked tokens and entries,
+entries that name one index twice, infinities and NaN, in place, offsets past
+32 bits, captured and on two streams."""
+import math
+
+import pytest
+import torch
+
+from gpu_util import torch_cuda
+from rows_util import check_distill, distill_64, gaps_untouched, matrix
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+VOCABS = [1, 2, 7, 8, 9, 64, 255, 257, 1000, 2048, 2051, 4099, 8192, 16381, 32000, 50257, 131072, 150001]
+
+
+@pytest.fixture(scope="module")
+def ddp():
+    torch_cuda()
+    import gradient_allreduce_averaging_amd as ddp
+    return ddp
+
+
+def _case(seed, rows, vocab, top, dtype, tdt="f32", idt=torch.int64, pad=0, shift=0, short=False):
+    """Per-rank logits, teacher logits and indices (distinct in a token, where the vocabulary
+    has that many)."""
+    g = torch.Generator().manual_seed(seed)
+    z, t, i = [], [], []
+    for n in rows:
+        zz = 3.0 * torch.randn(n, vocab, generator=g)
+        z.append(matrix(zz.to(DT[dtype]), pad, shift))
+        tt = (4.0 * torch.randn(n, top, generator=g)).to(DT[tdt])
+        if top <= vocab:
+            ii = torch.stack([torch.randperm(vocab, generator=g)[:top] for _ in range(n)]) if n \
+                else torch.zeros(0, top, dtype=torch.int64)
+        else:
+            ii = torch.randint(0, vocab, (n, top), generator=g)
+        if short and n:
+            keep = torch.randint(0, top + 1, (n, 1), generator=g)
+            gone = torch.arange(top)[None] >= keep
+            ii = ii.masked_fill(gone, -1)
+            tt = tt.masked_fill(gone, math.nan)
+        t.append(matrix(tt, pad, shift))
+        i.append(matrix(ii.to(idt), pad, shift))
+    return z, t, i
+
+
+def _run(ddp, z, t, i, weight=None, tau=1.0, scale=1.0, grad=True, dz=None, check=True, what=""):
+    loss = torch.full((1,), math.nan, device="cuda")
+    rl = [torch.full((x.shape[0],), math.nan, device="cuda") for x in z]
+    if not grad:
+        ddp.distill_loss(z, t, i, loss, row_loss=rl, token_weight=weight, temperature=tau)
+        if check:
+            check_distill(loss, rl, None, z, t, i, weight, tau, what=what)
+        return loss, rl, None
+    old = [x.clone() for x in z]
+    dz = [torch.empty_like(x) for x in z] if dz is None else dz
+    ddp.distill_grad(z, t, i, dz, loss, row_loss=rl, token_weight=weight, temperature=tau, grad_scale=scale)
+    if check:
+        check_distill(loss, rl, dz, old, t, i, weight, tau, scale, what)
+    return loss, rl, dz
+
+
+@pytest.mark.parametrize("vocab", VOCABS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_vocabularies(ddp, vocab, dtype):
+    for k, (rows, top) in enumerate((([2, 0, 1, 3], 8), ([1], 1), ([9], 37), ([2], 300))):
+        pad, shift = [(0, 0), (5, 1), (8, 3), (1, 7)][(k + vocab) % 4]
+        z, t, i = _case(k, rows, vocab, top, dtype, "bf16" if k == 2 else "f32",
+                        torch.int32 if k % 2 else torch.int64, pad, shift, short=k == 2)
+        tau = [1.0, 2.0, 0.7, 3.5][k]
+        what = (vocab, dtype, rows, top)
+        a = _run(ddp, z, t, i, tau=tau, grad=False, what=what)
+        dz = [matrix(torch.zeros_like(x).cpu(), pad, shift) for x in z]
+        b = _run(ddp, z, t, i, tau=tau, scale=0.5, dz=dz, what=what)
+        for x, y in zip(a[1], b[1]):
+            assert torch.equal(x, y), what
+        for d in dz:
+            assert gaps_untouched(d), what
+
+
+@pytest.mark.parametrize("rows", [[1], [2], [5, 3], [31], [64, 1, 64], [300], [129] * 8])
+@pytest.mark.parametrize("vocab", [1000, 32000, 50257])
+def test_token_counts_with_masks(ddp, rows, vocab):
+    z, t, i = _case(len(rows), rows, vocab, 24, "bf16", short=True)
+    g = torch.Generator().manual_seed(1)
+    weight = []
+    for n in rows:
+        w = torch.rand(n, generator=g) + 0.1
+        w[torch.rand(n, generator=g) < 0.3] = 0.0
+        weight.append(w.cuda())
+    for grad in (False, True):
+        _run(ddp, z, t, i, weight, 1.5, grad=grad, what=(rows, vocab))
+
+
+@pytest.mark.parametrize("vocab", [100, 32000])
+def test_tokens_that_are_not_live_are_not_looked_at(ddp, vocab):
+    rows, top = [6, 4], 5
+    z, t, i = _case(3, rows, vocab, top, "f32")
+    w = [torch.ones(n, device="cuda") for n in rows]
+    z[0][0] = math.nan                  # weight 0
+    w[0][0] = 0.0
+    w[0][1] = math.nan                  # a weight that is no number
+    z[0][1] = math.inf
+    w[1][0] = -3.0
+    i[0][2] = -1                        # no entry
+    t[0][2] = math.nan
+    z[0][2] = math.nan
+    t[1][1] = -math.inf                 # every entry of no probability
+    z[1][1] = math.nan
+    i[1][2, :3] = torch.tensor([vocab, vocab + 5, 2 ** 62])   # out of range
+    t[1][2, :3] = math.nan
+    i[0][3, 0] = -2 ** 63
+    loss, rl, dz = _run(ddp, z, t, i, w, 2.0)
+    assert torch.isfinite(loss).all()
+    for r, k in ((0, 0), (0, 1), (0, 2), (1, 0), (1, 1)):
+        assert rl[r][k] == 0 and (dz[r][k] == 0).all()
+    _run(ddp, z, t, i, w, 2.0, grad=False)
+
+
+def test_no_live_token_at_all(ddp):
+    z, t, i = _case(0, [3, 2], 1000, 4, "bf16")
+    w = [torch.zeros(3, device="cuda"), torch.zeros(2, device="cuda")]
+    for grad in (False, True):
+        loss, rl, dz = _run(ddp, z, t, i, w, grad=grad, check=False)
+        assert loss == 0 and all((x == 0).all() for x in rl)
+        assert dz is None or all((d == 0).all() for d in dz)
+    none = [torch.empty(0, 50, device="cuda")]
+    loss = torch.full((1,), 3.0, device="cuda")
+    ddp.distill_grad(none, [torch.empty(0, 4, device="cuda")], [torch.empty(0, 4, device="cuda", dtype=torch.int32)],
+                     [torch.empty(0, 50, device="cuda")], loss)
+    assert loss == 0
+    loss.fill_(3.0)
+    ddp.distill_loss(none, [torch.empty(0, 4, device="cuda")], [torch.empty(0, 4, device="cuda", dtype=torch.int32)],
+                     loss)
+    assert loss == 0
+
+
+@pytest.mark.parametrize("vocab", [9, 5000, 60000])
+@pytest.mark.parametrize("top", [6, 1024])
+def test_an_index_named_twice(ddp, vocab, top):
+    z, t, i = _case(1, [3, 2], vocab, top, "f32")
+    for x in i:
+        x[:, 1] = x[:, 0]
+        x[:, -1] = x[:, 0]
+        if top > 100:
+            x[:, 50:90] = x[:, 20:60]
+    _run(ddp, z, t, i, tau=1.3)
+    _run(ddp, z, t, i, tau=1.3, grad=False)
+
+
+@pytest.mark.parametrize("vocab", [33, 4096, 50257])
+def test_unusual_logits(ddp, vocab):
+    rows, top = [8], 4
+    z, t, i = _case(2, rows, vocab, top, "f32")
+    z, t, i = z[0], t[0], i[0]
+    # half of the vocabulary forbidden, the teacher's entries aside
+    keep = z[0].gather(0, i[0])
+    z[0, ::2] = -math.inf
+    z[0].scatter_(0, i[0], keep)
+    # all but the entries at the type's lowest value
+    keep = z[1].gather(0, i[1])
+    z[1] = torch.finfo(torch.float32).min
+    z[1].scatter_(0, i[1], keep)
+    z[2] = torch.finfo(torch.float32).min          # every logit at the lowest value
+    z[3] = 7e37                                    # and at a large one
+    z[4, vocab // 2] = math.nan
+    z[5] = -math.inf
+    z[6, i[6, 0]] = -math.inf                      # a teacher's entry that the student forbids
+    t[7] = torch.finfo(torch.float32).min          # teacher's entries all equal and lowest
+    ones = torch.ones(8, device="cuda")
+    for row in (0, 1, 2, 3, 7):
+        _run(ddp, [z[row:row + 1]], [t[row:row + 1]], [i[row:row + 1]], what=row)
+    loss, rl, dz = _run(ddp, [z], [t], [i], [ones], check=False)
+    assert torch.isnan(rl[0][4]) and torch.isnan(rl[0][5]) and rl[0][6] == math.inf
+    assert torch.isnan(dz[0][4]).all() and torch.isnan(dz[0][5]).all()
+    assert torch.isfinite(dz[0][[0, 1, 2, 3, 6, 7]]).all()
+    assert torch.isfinite(rl[0][[0, 1, 2, 3, 7]]).all()
+    # q is 0 at the forbidden entry: its gradient is that of the teacher's share alone
+    _, _, want, _, _, _ = distill_64([z[6:7]], [t[6:7]], [i[6:7]], None, 1.0)
+    got = dz[0][6].double() * 8
+    assert ((got - want[0][0]).abs() <= 1e-4 * (want[0][0].abs() + 1e-3)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [([2], 1000), ([3, 2], 50257), ([200], 32000), ([2], 150001)])
+def test_in_place(ddp, dtype, rows, vocab):
+    z, t, i = _case(5, rows, vocab, 16, dtype)
+    for x in i:
+        x[:, 1] = x[:, 0]
+    _, rl, want = _run(ddp, z, t, i, tau=2.0)
+    _, rl2, got = _run(ddp, z, t, i, tau=2.0, dz=z, check=False)
+    assert got[0] is z[0]
+    for a, b in zip(want + rl, got + rl2):
+        assert torch.equal(a, b)
+
+
+def test_average_over_ranks_is_the_gradient_of_the_whole(ddp):
+    """Ranks with unequal numbers of live tokens: the 1/N average of what follows from dlogits
+    is the gradient of the mean over all tokens, in 64 bits by autograd."""
+    vocab, width, top, rows, tau = 500, 16, 6, [7, 2, 0, 5], 2.0
+    g = torch.Generator().manual_seed(0)
+    w64 = torch.randn(vocab, width, generator=g, dtype=torch.float64, requires_grad=True)
+    hs = [torch.randn(n, width, generator=g, dtype=torch.float64) for n in rows]
+    ts = [torch.randn(n, top, generator=g) for n in rows]
+    idx = [torch.stack([torch.randperm(vocab, generator=g)[:top] for _ in range(n)]) if n
+           else torch.zeros(0, top, dtype=torch.int64) for n in rows]
+    live = [torch.arange(n) % 3 != 1 for n in rows]
+    total, count = 0.0, 0
+    for h, t, i, on in zip(hs, ts, idx, live):
+        logq = torch.log_softmax(h @ w64.t() / tau, 1)
+        logp = torch.log_softmax(t.double() / tau, 1)
+        kl = (logp.exp() * (logp - logq.gather(1, i))).sum(1) * tau * tau
+        total, count = total + kl[on].sum(), count + int(on.sum())
+    (total / count).backward()
+    z = [(h @ w64.detach().t()).float().cuda() for h in hs]
+    dz = [torch.empty_like(x) for x in z]
+    loss = torch.empty(1, device="cuda")
+    ddp.distill_grad(z, [t.cuda() for t in ts], [i.cuda() for i in idx], dz, loss,
+                     token_weight=[o.float().cuda() for o in live], temperature=tau)
+    # each rank's weight gradient in the flat layout, averaged by the sync
+    plan = ddp.plan_buckets([vocab * width], 25 << 20)
+    flats = [(d.double().cpu().t() @ h).float().reshape(-1).cuda() for d, h in zip(dz, hs)]
+    out = torch.empty(plan.total, device="cuda")
+    ddp.sync_allreduce_avg(plan, flats, out, "ring")
+    want = w64.grad.reshape(-1)
+    scale = float(want.abs().max())
+    # dz in f32 off by well under 1e-5 of q + p <= 2 a row, 14 rows of h about 1
+    assert (out.double().cpu() - want).abs().max() <= 1e-4 * scale
+    assert abs(float(loss) - float(total.detach()) / count) <= 1e-5 * float(total.detach()) / count
+
+
+def test_gradient_matches_differences(ddp):
+    vocab, top, rows, tau = 700, 9, [3, 2], 1.7
+    z, t, i = _case(7, rows, vocab, top, "f32")
+    loss, _, dz = _run(ddp, z, t, i, tau=tau)
+    g = torch.Generator().manual_seed(3)
+    for _ in range(4):
+        v = [torch.randn(n, vocab, generator=g).cuda() for n in rows]
+        h = 2.0 ** -6
+        far = []
+        for sign in (1, -1):
+            far.append(float(_run(ddp, [a + sign * h * b for a, b in zip(z, v)], t, i, tau=tau, grad=False,
+                                  check=False)[0]))
+        num = (far[0] - far[1]) / (2 * h) * len(rows)
+        want = sum(float((a.double() * b.double()).sum()) for a, b in zip(dz, v))
+        size = sum(float((a.double() * b.double()).abs().sum()) for a, b in zip(dz, v))
+        # a term of h^2 times third derivatives (each at most about the first), f32 losses over h
+        assert abs(num - want) <= size * 4 * h * h + float(loss) * len(rows) * 2.0 ** -18 / h
+
+
+def test_offsets_past_32_bits(ddp):
+    vocab, far = 3000, (1 << 31) + 8
+    z, t, i = _case(0, [3], vocab, 8, "bf16")
+    buf = torch.empty(2 * far + vocab + 16, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((3, vocab), (far, 1), 3)
+    x.copy_(z[0])
+    _, rl, dz = _run(ddp, z, t, i)
+    _, rl2, _ = _run(ddp, [x], t, i, dz=[x], check=False)
+    assert torch.equal(x, dz[0]) and torch.equal(rl[0], rl2[0])
+
+
+def test_captured_and_replayed(ddp):
+    """Two graphs, each with a workspace of its own, replayed in turn with new values between."""
+    shapes = [([40, 3], 5003, 7), ([2], 50257, 20)]
+    sets, graphs = [], []
+    for rows, vocab, top in shapes:
+        z, t, i = _case(0, rows, vocab, top, "bf16")
+        n_loss, rl = torch.empty(1, device="cuda"), [torch.empty(n, device="cuda") for n in rows]
+        dz = [torch.empty_like(x) for x in z]
+        ws = torch.empty(ddp.distill_workspace(rows, vocab), dtype=torch.uint8, device="cuda")
+        sets.append((z, t, i, n_loss, rl, dz, ws))
+
+    def step(k):
+        z, t, i, loss, rl, dz, ws = sets[k]
+        ddp.distill_grad(z, t, i, dz, loss, row_loss=rl, temperature=2.0, workspace=ws)
+
+    for k in range(2):
+        step(k)
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(gr, stream=st):
+            step(k)
+        graphs.append(gr)
+    torch.cuda.synchronize()
+    for rep in range(4):
+        for k, (rows, vocab, top) in enumerate(shapes):
+            z, t, i = _case(10 + rep, rows, vocab, top, "bf16", short=rep % 2 == 1)
+            for dst, src in zip(sets[k][0] + sets[k][1] + sets[k][2], z + t + i):
+                dst.copy_(src)
+        torch.cuda.synchronize()
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        got = [[x.clone() for x in [s[3]] + s[4] + s[5]] for s in sets]
+        for k in range(2):
+            step(k)
+        torch.cuda.synchronize()
+        for s, g in zip(sets, got):
+            for a, b in zip(g, [s[3]] + s[4] + s[5]):
+                assert torch.equal(a, b), rep
+
+
+def test_two_streams_at_once(ddp):
+    cases = [_case(k, [60], 32000, 16, "bf16") for k in range(2)]
+    want = [_run(ddp, *c, check=False) for c in cases]
+    outs = [(torch.empty(1, device="cuda"), [torch.empty_like(c[0][0])]) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for c, o, st in zip(cases, outs, streams):
+            ddp.distill_grad(*c, o[1], o[0], stream=st)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert torch.equal(w[0], o[0]) and torch.equal(w[2][0], o[1][0])
+
+
+def test_python_refusals(ddp):
+    z, t, i = _case(0, [3], 50, 4, "f32")
+    loss = torch.empty(1, device="cuda")
+    with pytest.raises(ValueError):
+        ddp.distill_grad(z, t, i, None, loss)
+    with pytest.raises(ValueError):
+        ddp.distill_grad(z, t, i, [torch.empty(3, 49, device="cuda")], loss)
+    with pytest.raises(ValueError):
+        ddp.distill_grad(z, t, i, [torch.empty(3, 50, device="cuda", dtype=torch.bfloat16)], loss)
+    with pytest.raises(ValueError):
+        ddp.distill_loss(z, t, [i[0][:, :3]], loss)
+    with pytest.raises(TypeError):
+        ddp.distill_loss(z, t, [i[0].to(torch.int16)], loss)
+    with pytest.raises(TypeError):
+        ddp.distill_loss(z, t, i, loss.double())
+    with pytest.raises(ValueError):
+        ddp.distill_loss(z, t, i, torch.empty(2, device="cuda"))
+    with pytest.raises(ValueError):
+        ddp.distill_loss(z, t, i, loss, token_weight=[torch.ones(2, device="cuda")])
+    with pytest.raises(TypeError):
+        ddp.distill_loss(z, t, i, loss, token_weight=[torch.ones(3, device="cuda", dtype=torch.float64)])
+    with pytest.raises(ddp.DDPError):
+        ddp.distill_loss(z, t, i, loss, temperature=0.0)
+    with pytest.raises(ddp.DDPError):
+        ddp.distill_loss(z, t, i, loss, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        ddp.distill_loss(z, t, i, loss.cpu())

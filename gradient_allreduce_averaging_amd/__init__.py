@@ -20,6 +20,8 @@ import ctypes
 import os
 from typing import List, Optional, Sequence
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libddp.so")
 
@@ -44,11 +46,6 @@ class DDPError(RuntimeError):
         self.status = status
         msg = f"{call} failed: {STATUS.get(status, status)}"
         super().__init__(msg + (f" ({detail})" if detail else ""))
-
-
-class _RowsC(ctypes.Structure):
-    """ddp_rows_t."""
-    _fields_ = [("rank", ctypes.c_void_p), ("stride", ctypes.c_int64)]
 
 
 def _hip_runtimes_mapped():
@@ -76,7 +73,6 @@ def _load():
     c_i64p = ctypes.POINTER(ctypes.c_int64)
     c_i32p = ctypes.POINTER(ctypes.c_int32)
     vp = ctypes.c_void_p
-    rp = ctypes.POINTER(_RowsC)
     sig = {
         "ddp_plan_buckets": ([c_i64p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int,
                               ctypes.POINTER(vp)], ctypes.c_int),
@@ -123,20 +119,20 @@ def _load():
                                        ctypes.c_float, vp], ctypes.c_int),
         "ddp_accumulate": ([ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.c_int32, ctypes.c_int64,
                             ctypes.c_int, vp], ctypes.c_int),
-        "ddp_rms_norm": ([c_i64p, ctypes.c_int32, ctypes.c_int64, rp, rp, ctypes.c_int, vp,
-                          ctypes.c_int, ctypes.c_float, rp, rp, ctypes.c_int, vp, vp],
+        "ddp_rms_norm": ([vp, ctypes.c_int32, ctypes.c_int64, vp, vp, ctypes.c_int, vp,
+                          ctypes.c_int, ctypes.c_float, vp, vp, ctypes.c_int, vp, vp],
                          ctypes.c_int),
-        "ddp_rms_norm_grad": ([c_i64p, ctypes.c_int32, ctypes.c_int64, rp, ctypes.c_int, vp,
-                               ctypes.c_int, ctypes.c_float, rp, ctypes.c_int, rp, rp, vp,
+        "ddp_rms_norm_grad": ([vp, ctypes.c_int32, ctypes.c_int64, vp, ctypes.c_int, vp,
+                               ctypes.c_int, ctypes.c_float, vp, ctypes.c_int, vp, vp, vp,
                                ctypes.c_int, ctypes.c_int32, vp, ctypes.c_int64, vp],
                               ctypes.c_int),
         "ddp_rms_norm_grad_workspace": ([c_i64p, ctypes.c_int32, ctypes.c_int64], ctypes.c_int64),
-        "ddp_distill_loss": ([c_i64p, ctypes.c_int32, ctypes.c_int64, rp, ctypes.c_int,
-                              ctypes.c_int32, rp, ctypes.c_int, rp, ctypes.c_int32, vp,
+        "ddp_distill_loss": ([vp, ctypes.c_int32, ctypes.c_int64, vp, ctypes.c_int,
+                              ctypes.c_int32, vp, ctypes.c_int, vp, ctypes.c_int32, vp,
                               ctypes.c_float, vp, vp, vp, ctypes.c_int64, vp], ctypes.c_int),
-        "ddp_distill_grad": ([c_i64p, ctypes.c_int32, ctypes.c_int64, rp, ctypes.c_int,
-                              ctypes.c_int32, rp, ctypes.c_int, rp, ctypes.c_int32, vp,
-                              ctypes.c_float, ctypes.c_float, rp, vp, vp, vp, ctypes.c_int64, vp],
+        "ddp_distill_grad": ([vp, ctypes.c_int32, ctypes.c_int64, vp, ctypes.c_int,
+                              ctypes.c_int32, vp, ctypes.c_int, vp, ctypes.c_int32, vp,
+                              ctypes.c_float, ctypes.c_float, vp, vp, vp, vp, ctypes.c_int64, vp],
                              ctypes.c_int),
         "ddp_distill_workspace": ([c_i64p, ctypes.c_int32, ctypes.c_int64], ctypes.c_int64),
         "ddp_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -600,122 +596,155 @@ def accumulate(dst: Sequence, src: Sequence, length: Optional[int] = None, strea
 
 # ---------------------------------------------------------------- rows of tokens
 
-class _Tokens:
-    """The shape of one call's matrices, and every rank's tensors as the C
-    call takes them.  ``like[r]`` is rank r's matrix: [..., width], its rows one
-    fixed distance apart."""
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+_NORM_OUT = {**_FLOATS, torch.int8: I8, torch.float8_e4m3fn: E4M3}
+_INDICES = {torch.int32: 4, torch.int64: 8}
+_ONE_F32 = {torch.float32: F32}
 
-    def __init__(self, like: Sequence, width: Optional[int] = None):
-        import torch
-        self.torch = torch
+
+class _Tokens:
+    """The operands of one call over every rank's rows of tokens, checked and
+    laid out as the C call takes them.  ``like[r]`` is rank r's matrix [..., width],
+    its rows one fixed distance apart; the other operands have its shape.
+
+    All pointer arrays and ddp_rows_t structures of a call go into one buffer of
+    64-bit words: an operand is known by its place there (``ref``) until ``done`` makes the
+    buffer."""
+
+    def __init__(self, like: Sequence):
         self.device = torch.cuda.current_device()
         self.n = len(like)
         if self.n == 0:
             raise ValueError("no ranks")
-        if like[0].dim() == 0:
-            raise ValueError("a rank's tensor needs a dimension of its own for the width")
-        self.width = like[0].shape[-1] if width is None else int(width)
-        if self.width < 1:
-            raise ValueError("the width is 0")
-        self.rows = [t.numel() // self.width for t in like]
-        self.c_rows = (ctypes.c_int64 * self.n)(*self.rows)
-        self._keep = []
+        self.rows = []
+        self.width = 0
+        for t in like:
+            shape = t.shape
+            if not shape:
+                raise ValueError("a rank's tensor needs a dimension for the width")
+            self.width = self.width or shape[-1]
+            if self.width < 1:
+                raise ValueError("the width is 0")
+            self.rows.append(shape[0] if len(shape) == 2 else t.numel() // self.width)
+        self.words = list(self.rows)
+        self.fix = []          # words that hold the address of another word
 
-    def check(self, t):
-        """Of this call's device."""
-        if not t.is_cuda:
-            raise ValueError("tensor is not on a GPU")
+    def _on_device(self, t):
         if t.get_device() != self.device:
-            raise ValueError("tensor is not on the current GPU")
+            raise ValueError("tensor is not on the current GPU" if t.is_cuda else "tensor is not on a GPU")
 
-    def matrix(self, ts, what: str, dtypes, width: Optional[int] = None):
-        """(dtype, ddp_rows_t) of one operand; None, None where it is absent."""
+    def matrix(self, ts, what: str, codes, width: int):
+        """(dtype, ref of its ddp_rows_t) of one operand; (None, None) where it is absent."""
         if ts is None:
             return None, None
-        width = self.width if width is None else width
         if len(ts) != self.n:
             raise ValueError(f"{what}: one tensor per rank is required")
-        dtype, stride = ts[0].dtype, None
-        if dtype not in dtypes:
+        dtype, stride, device, words = ts[0].dtype, None, self.device, self.words
+        if dtype not in codes:
             raise TypeError(f"{what}: unsupported dtype {dtype}")
-        ptrs = []
+        first = len(words)
         for t, n in zip(ts, self.rows):
-            self.check(t)
+            if t.get_device() != device:
+                self._on_device(t)
             if t.dtype != dtype:
                 raise ValueError(f"{what}: the ranks differ in dtype")
-            if t.dim() == 0 or t.shape[-1] != width or t.numel() != n * width:
-                raise ValueError(f"{what}: {n} rows of {width} elements are required, "
-                                 f"got {tuple(t.shape)}")
-            if n > 0 and width > 1 and t.stride(-1) != 1:
-                raise ValueError(f"{what}: the elements of a row are not consecutive")
-            if n > 1:
-                if t.dim() == 2:
-                    st = t.stride(0)
-                else:
+            shape = t.shape
+            if len(shape) == 2:
+                fits = shape[0] == n and shape[1] == width
+                strides = t.stride()
+            else:
+                fits = len(shape) > 0 and shape[-1] == width and t.numel() == n * width
+                strides = None
+            if not fits:
+                raise ValueError(f"{what}: {n} rows of {width} elements are required, got {tuple(shape)}")
+            if n > 0:
+                if strides is None:
                     try:
-                        st = t.view(-1, width).stride(0)
+                        strides = t.view(-1, width).stride()
                     except RuntimeError:
                         raise ValueError(f"{what}: the rows are not one fixed distance apart") from None
-                if stride is not None and st != stride:
-                    raise ValueError(f"{what}: the ranks differ in row stride")
-                stride = st
-            ptrs.append(t.data_ptr())
-        arr = (ctypes.c_void_p * self.n)(*ptrs)
-        self._keep.append(arr)
-        return dtype, _RowsC(ctypes.addressof(arr), width if stride is None else stride)
+                if width > 1 and strides[1] != 1:
+                    raise ValueError(f"{what}: the elements of a row are not consecutive")
+                if n > 1:
+                    if stride is None:
+                        stride = strides[0]
+                    elif stride != strides[0]:
+                        raise ValueError(f"{what}: the ranks differ in row stride")
+            words.append(t.data_ptr())
+        self.fix.append((len(words), first))
+        words.append(0)
+        words.append(width if stride is None else stride)
+        return dtype, len(words) - 2
 
-    def vectors(self, ts, what: str, length=None, dtypes=None):
-        """(dtype, pointer array) of one vector per rank: ``length`` elements, or one for
-        each of the rank's rows."""
+    def vectors(self, ts, what: str, length=None, codes=_ONE_F32):
+        """(dtype, ref of the pointer array) of one vector per rank: ``length`` elements, or one
+        for each of the rank's rows."""
         if ts is None:
             return None, None
         if len(ts) != self.n:
             raise ValueError(f"{what}: one tensor per rank is required")
-        dtype = ts[0].dtype
-        if dtype not in (dtypes or (self.torch.float32,)):
+        dtype, first = ts[0].dtype, len(self.words)
+        if dtype not in codes:
             raise TypeError(f"{what}: unsupported dtype {dtype}")
         for t, n in zip(ts, self.rows):
-            self.check(t)
+            self._on_device(t)
             if t.dtype != dtype:
                 raise ValueError(f"{what}: the ranks differ in dtype")
-            if t.numel() != (n if length is None else length):
-                raise ValueError(f"{what}: {n if length is None else length} elements are required, "
-                                 f"got {t.numel()}")
+            want = n if length is None else length
+            if t.numel() != want:
+                raise ValueError(f"{what}: {want} elements are required, got {t.numel()}")
             if not t.is_contiguous():
                 raise ValueError(f"{what}: tensor is not contiguous")
-        return dtype, (ctypes.c_void_p * self.n)(*[t.data_ptr() for t in ts])
+            self.words.append(t.data_ptr())
+        return dtype, first
 
-    def shared(self, t, what: str, length: int):
-        """Address of a tensor every rank shares."""
-        self.check(t)
+    def shared(self, t, what: str, length: int, codes):
+        """(dtype code, address) of a tensor every rank shares; (F32, None) where it is absent."""
+        if t is None:
+            return F32, None
+        self._on_device(t)
+        if t.dtype not in codes:
+            raise TypeError(f"{what}: unsupported dtype {t.dtype}")
         if t.numel() != length:
             raise ValueError(f"{what}: {length} elements are required, got {t.numel()}")
         if not t.is_contiguous():
             raise ValueError(f"{what}: tensor is not contiguous")
-        return t.data_ptr()
+        return codes[t.dtype], t.data_ptr()
 
-    def workspace(self, t, need: int, stream):
-        """(address, bytes, tensor) of the caller's workspace, or of a new one that belongs to
-        the call's stream."""
-        if need < 0:
-            raise DDPError(1, "workspace")
-        torch = self.torch
+    def workspace(self, t, need, stream):
+        """(address, bytes, tensor) of the caller's workspace, or of a new one of need(rows, n,
+        width) bytes that belongs to the call's stream."""
         if t is None:
+            nbytes = need((ctypes.c_int64 * self.n)(*self.rows), self.n, self.width)
+            if nbytes < 0:
+                raise DDPError(1, need.__name__)
             if stream is None:
-                t = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+                t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
             else:
                 s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
                 with torch.cuda.stream(s):
-                    t = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
-        else:
-            self.check(t)
-            if not t.is_contiguous():
-                raise ValueError("workspace: tensor is not contiguous")
+                    t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+            return t.data_ptr(), nbytes, t
+        self._on_device(t)
+        if not t.is_contiguous():
+            raise ValueError("workspace: tensor is not contiguous")
         return t.data_ptr(), t.numel() * t.element_size(), t
 
+    def stream(self, stream) -> int:
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device)
+        return _stream_handle(stream)
 
-def _float_codes(torch):
-    return {torch.float32: F32, torch.bfloat16: BF16}
+    def done(self, *refs):
+        """The buffer (to be kept until the call returns) and the address of each ref, None for
+        None; ref 0 is the row counts."""
+        buf = (ctypes.c_int64 * len(self.words))()
+        base = ctypes.addressof(buf)
+        words = self.words
+        for at, first in self.fix:
+            words[at] = base + 8 * first
+        buf[:] = words
+        return buf, [None if r is None else base + 8 * r for r in refs]
 
 
 def rms_norm(x: Sequence, weight, out: Sequence, residual: Optional[Sequence] = None,
@@ -725,38 +754,33 @@ def rms_norm(x: Sequence, weight, out: Sequence, residual: Optional[Sequence] = 
     residual[r], for every rank in one launch (``ddp_rms_norm``).  ``sum_out``
     receives s; an int8 or float8_e4m3fn ``out`` comes with ``scale``, one f32 per row."""
     tk = _Tokens(x)
-    torch = tk.torch
-    codes = _float_codes(torch)
-    dt, xr = tk.matrix(x, "x", codes)
-    codes8 = {**codes, torch.int8: I8, torch.float8_e4m3fn: E4M3}
-    ydt, yr = tk.matrix(out, "out", codes8)
-    rdt, rr = tk.matrix(residual, "residual", codes)
-    sdt, sr = tk.matrix(sum_out, "sum_out", codes)
-    if rdt not in (None, dt) or sdt not in (None, dt):
+    width = tk.width
+    dt, xr = tk.matrix(x, "x", _FLOATS, width)
+    ydt, yr = tk.matrix(out, "out", _NORM_OUT, width)
+    rdt, rr = tk.matrix(residual, "residual", _FLOATS, width)
+    sdt, sr = tk.matrix(sum_out, "sum_out", _FLOATS, width)
+    if (rdt or dt) != dt or (sdt or dt) != dt:
         raise ValueError("residual and sum_out must have x's dtype")
     _, sc = tk.vectors(scale, "scale")
-    wp, wdt = None, F32
-    if weight is not None:
-        wp = tk.shared(weight, "weight", tk.width)
-        if weight.dtype not in codes:
-            raise TypeError(f"weight: unsupported dtype {weight.dtype}")
-        wdt = codes[weight.dtype]
-    _check(lib.ddp_rms_norm(tk.c_rows, tk.n, tk.width, xr, rr, codes[dt], wp, wdt, eps, sr, yr,
-                            codes8[ydt], sc, _stream_handle(stream)), "ddp_rms_norm")
+    wdt, wp = tk.shared(weight, "weight", width, _FLOATS)
+    buf, (rows, xr, rr, sr, yr, sc) = tk.done(0, xr, rr, sr, yr, sc)
+    st = lib.ddp_rms_norm(rows, tk.n, width, xr, rr, _FLOATS[dt], wp, wdt, eps, sr, yr, _NORM_OUT[ydt], sc,
+                          tk.stream(stream))
+    if st:
+        _check(st, "ddp_rms_norm")
 
 
-def _rows_of(rows):
-    rows = [int(n) for n in rows]
-    return (ctypes.c_int64 * len(rows))(*rows), len(rows)
+def _workspace_bytes(fn, rows: Sequence[int], width: int) -> int:
+    n = len(rows)
+    need = fn((ctypes.c_int64 * n)(*rows), n, int(width))
+    if need < 0:
+        raise DDPError(1, fn.__name__)
+    return need
 
 
 def rms_norm_grad_workspace(rows: Sequence[int], width: int) -> int:
     """Bytes of workspace ``rms_norm_grad`` needs for ranks of ``rows[r]`` rows."""
-    c, n = _rows_of(rows)
-    need = lib.ddp_rms_norm_grad_workspace(c, n, int(width))
-    if need < 0:
-        raise DDPError(1, "ddp_rms_norm_grad_workspace")
-    return need
+    return _workspace_bytes(lib.ddp_rms_norm_grad_workspace, rows, width)
 
 
 def rms_norm_grad(s: Sequence, weight, dy: Sequence, dx: Sequence, dsum: Optional[Sequence] = None,
@@ -766,69 +790,59 @@ def rms_norm_grad(s: Sequence, weight, dy: Sequence, dx: Sequence, dsum: Optiona
     s[r] (so of x and the residual), dweight[r] the rank's weight gradient, stored or, with
     ``accumulate``, added to what is there."""
     tk = _Tokens(s)
-    torch = tk.torch
-    codes = _float_codes(torch)
-    dt, sr = tk.matrix(s, "s", codes)
-    ydt, yr = tk.matrix(dy, "dy", codes)
-    ddt, dr = tk.matrix(dsum, "dsum", codes)
-    xdt, xr = tk.matrix(dx, "dx", codes)
-    if xdt != dt or ddt not in (None, dt):
+    width = tk.width
+    dt, sr = tk.matrix(s, "s", _FLOATS, width)
+    ydt, yr = tk.matrix(dy, "dy", _FLOATS, width)
+    ddt, dr = tk.matrix(dsum, "dsum", _FLOATS, width)
+    xdt, xr = tk.matrix(dx, "dx", _FLOATS, width)
+    if xdt != dt or (ddt or dt) != dt:
         raise ValueError("dx and dsum must have s's dtype")
-    wp, wdt = None, F32
-    if weight is not None:
-        wp = tk.shared(weight, "weight", tk.width)
-        if weight.dtype not in codes:
-            raise TypeError(f"weight: unsupported dtype {weight.dtype}")
-        wdt = codes[weight.dtype]
-    wgdt, wg = tk.vectors(dweight, "dweight", tk.width, codes)
+    wdt, wp = tk.shared(weight, "weight", width, _FLOATS)
+    gdt, wg = tk.vectors(dweight, "dweight", width, _FLOATS)
     ws, nbytes, keep = None, 0, None
     if dweight is not None:
-        need = lib.ddp_rms_norm_grad_workspace(tk.c_rows, tk.n, tk.width) if workspace is None else 0
-        ws, nbytes, keep = tk.workspace(workspace, need, stream)
-    _check(lib.ddp_rms_norm_grad(tk.c_rows, tk.n, tk.width, sr, codes[dt], wp, wdt, eps, yr,
-                                 codes[ydt], dr, xr, wg, codes.get(wgdt, F32),
-                                 1 if accumulate else 0, ws, nbytes, _stream_handle(stream)),
-           "ddp_rms_norm_grad")
+        ws, nbytes, keep = tk.workspace(workspace, lib.ddp_rms_norm_grad_workspace, stream)
+    buf, (rows, sr, yr, dr, xr, wg) = tk.done(0, sr, yr, dr, xr, wg)
+    st = lib.ddp_rms_norm_grad(rows, tk.n, width, sr, _FLOATS[dt], wp, wdt, eps, yr, _FLOATS[ydt], dr, xr, wg,
+                               F32 if gdt is None else _FLOATS[gdt], 1 if accumulate else 0, ws, nbytes,
+                               tk.stream(stream))
+    if st:
+        _check(st, "ddp_rms_norm_grad")
 
 
 def distill_workspace(rows: Sequence[int], vocab: int) -> int:
     """Bytes of workspace ``distill_loss`` and ``distill_grad`` need for ranks of
     ``rows[r]`` tokens."""
-    c, n = _rows_of(rows)
-    need = lib.ddp_distill_workspace(c, n, int(vocab))
-    if need < 0:
-        raise DDPError(1, "ddp_distill_workspace")
-    return need
+    return _workspace_bytes(lib.ddp_distill_workspace, rows, vocab)
 
 
 def _distill(logits, teacher, index, dlogits, loss, row_loss, token_weight, temperature, grad_scale,
              workspace, stream):
     tk = _Tokens(logits)
-    torch = tk.torch
-    codes = _float_codes(torch)
-    dt, zr = tk.matrix(logits, "logits", codes)
+    vocab = tk.width
+    dt, zr = tk.matrix(logits, "logits", _FLOATS, vocab)
     if len(teacher) != tk.n or teacher[0].dim() == 0:
         raise ValueError("teacher: one tensor per rank is required")
     top = teacher[0].shape[-1]
-    tdt, tr = tk.matrix(teacher, "teacher", codes, top)
-    idt, ir = tk.matrix(index, "index", (torch.int32, torch.int64), top)
+    tdt, tr = tk.matrix(teacher, "teacher", _FLOATS, top)
+    idt, ir = tk.matrix(index, "index", _INDICES, top)
     _, tw = tk.vectors(token_weight, "token_weight")
     _, rl = tk.vectors(row_loss, "row_loss")
-    lp = tk.shared(loss, "loss", 1)
-    if loss.dtype != torch.float32:
-        raise TypeError(f"loss: unsupported dtype {loss.dtype}")
-    need = lib.ddp_distill_workspace(tk.c_rows, tk.n, tk.width) if workspace is None else 0
-    ws, nbytes, keep = tk.workspace(workspace, need, stream)
-    head = (tk.c_rows, tk.n, tk.width, zr, codes[dt], top, tr, codes[tdt], ir,
-            4 if idt == torch.int32 else 8, tw, temperature)
-    tail = (lp, rl, ws, nbytes, _stream_handle(stream))
-    if dlogits is None:
-        _check(lib.ddp_distill_loss(*head, *tail), "ddp_distill_loss")
-        return
-    gdt, gr = tk.matrix(dlogits, "dlogits", codes)
-    if gdt != dt:
+    _, lp = tk.shared(loss, "loss", 1, _ONE_F32)
+    gdt, gr = tk.matrix(dlogits, "dlogits", _FLOATS, vocab)
+    if (gdt or dt) != dt:
         raise ValueError("dlogits must have the logits' dtype")
-    _check(lib.ddp_distill_grad(*head, grad_scale, gr, *tail), "ddp_distill_grad")
+    ws, nbytes, keep = tk.workspace(workspace, lib.ddp_distill_workspace, stream)
+    buf, (rows, zr, tr, ir, tw, rl, gr) = tk.done(0, zr, tr, ir, tw, rl, gr)
+    if dlogits is None:
+        st = lib.ddp_distill_loss(rows, tk.n, vocab, zr, _FLOATS[dt], top, tr, _FLOATS[tdt], ir,
+                                  _INDICES[idt], tw, temperature, lp, rl, ws, nbytes, tk.stream(stream))
+    else:
+        st = lib.ddp_distill_grad(rows, tk.n, vocab, zr, _FLOATS[dt], top, tr, _FLOATS[tdt], ir,
+                                  _INDICES[idt], tw, temperature, grad_scale, gr, lp, rl, ws, nbytes,
+                                  tk.stream(stream))
+    if st:
+        _check(st, "ddp_distill_loss" if dlogits is None else "ddp_distill_grad")
 
 
 def distill_loss(logits: Sequence, teacher: Sequence, index: Sequence, loss,

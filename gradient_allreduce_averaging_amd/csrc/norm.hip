@@ -1,10 +1,28 @@
 // Root-mean-square norm of a residual sum, and its backward
 // (ddp_rms_norm, ddp_rms_norm_grad).
+//
+//     s = x + residual;  rho = 1 / sqrt(mean(s^2) + eps);  y = s rho w
+//     dx = dsum + rho (w dy - s rho^2 mean(w dy s));  dw = sum over rows of dy s rho
+//
+// A few operations per element, so HBM bounds both: the forward reads x and
+// the residual and writes the sum and y, the backward reads s, dy and dsum and
+// writes dx.  Both hold a row in registers between the row's sums and its
+// outputs, so every tensor moves once.  rho is not stored by the forward: the
+// backward reads all of s anyway and sums its squares beside w dy s.
+//
+// Measured (rocprofv3, MI355X): 8 ranks x 2048 x 4096 bf16, forward with a
+// residual 537 MB in 87 us = 6.2 TB/s, backward 537 MB in 92 us + 4.8 us for
+// the weight gradients' second launch = 5.5 TB/s.
+//
+// Rounding: s is rounded to its dtype because the rounded sum is what the next
+// layers add to, and what the backward is given; y, dx and dw are rounded once
+// from f32; sums, rho and the partial weight gradients are f32.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "host.h"
 #include "row_device.h"
@@ -18,6 +36,7 @@ constexpr int kI8 = 2;
 constexpr int kE4M3 = 3;
 
 constexpr int kNormThreads = 256;
+constexpr int64_t kMostGridRows = 1 << 16;   // blocks to a rank of norm_rows, which step through its rows
 
 struct NormArgs {
     RowPtrs x, res, sum, y;
@@ -26,7 +45,7 @@ struct NormArgs {
     const char *weight;
     int64_t width;
     int wdt;
-    float eps;
+    float eps, inv_width;
 };
 
 // s of element j: the residual added in f32 and rounded to the dtype.
@@ -71,6 +90,61 @@ __device__ __forceinline__ Quant quant_of(float most)
     return q;
 }
 
+// Four codes, packed.
+template <int YT>
+__device__ __forceinline__ uint32_t codes_of(const float *y, const Quant &q)
+{
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = y[e] * q.up * q.inv;
+    uint32_t c = 0;
+    if (YT == kI8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c |= (uint32_t)code_of<kI8>(v[e]) << (8 * e);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fminf(fmaxf(v[e], -448.0f), 448.0f);
+        c = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+        c = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], (int)c, true);
+    }
+    return c;
+}
+
+// The weight's V elements at `at`: the loads (nothing waits for them) and the
+// values, ones without a weight.
+template <int V>
+struct Weight {
+    u32x4 lo, hi;
+    __device__ __forceinline__ void load(const char *w, int wdt, uint32_t at)
+    {
+        if (!w) return;
+        if (wdt == kF32) {
+            lo = ld_vec<false, u32x4>(w + at * 4);
+            if (V == 8) hi = ld_vec<false, u32x4>(w + at * 4 + 16);
+        } else if (V == 8) {
+            lo = ld_vec<false, u32x4>(w + at * 2);
+        } else {
+            const u32x2 t = ld_vec<false, u32x2>(w + at * 2);
+            lo[0] = t[0];
+            lo[1] = t[1];
+        }
+    }
+    __device__ __forceinline__ void values(const char *w, int wdt, float *y) const
+    {
+        if (!w) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] = 1.0f;
+        } else if (wdt == kF32) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] = __uint_as_float(e < 4 ? lo[e & 3] : hi[e & 3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                y[e] = __uint_as_float((e & 1) ? lo[e >> 1] & 0xffff0000u : lo[e >> 1] << 16);
+        }
+    }
+};
+
 template <int DT, int YT, bool RES>
 __global__ void __launch_bounds__(kNormThreads) norm_rows(NormArgs a)
 {
@@ -111,16 +185,110 @@ __global__ void __launch_bounds__(kNormThreads) norm_rows(NormArgs a)
     }
 }
 
+// The row in registers: a block of up to 16 waves owns a row, each thread NV
+// 16-byte vectors of it (vector i of thread t is the row's vector
+// i * threads + t), so x (and the residual) are read once and every output is
+// written once.
+template <int DT, int YT, bool RES, int NV, bool NT>
+__global__ void __launch_bounds__(kMostWaves * kWave) norm_held(NormArgs a, int64_t first_row)
+{
+    constexpr int V = kVec<DT>, size = kSize<DT>;
+    constexpr bool k8 = YT == kI8 || YT == kE4M3;
+    __shared__ float lds[2 * kMostWaves];
+    int turn = 0;
+    const int r = blockIdx.y, threads = blockDim.x, waves = threads / kWave;
+    const int64_t row = first_row + blockIdx.x;
+    if (row >= a.rows[r]) return;
+    const char *x = a.x.p[r] + row * a.x.pitch;
+    const char *res = RES ? a.res.p[r] + row * a.res.pitch : nullptr;
+    Piece pc[NV];
+    u32x4 s[NV], q[NV];
+    Weight<V> wt[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        pc[i] = piece_of<V>(i * threads + (int)threadIdx.x, (int)a.width);
+        s[i] = ld_vec<NT, u32x4>(x + pc[i].at * size);
+        if (RES) q[i] = ld_vec<NT, u32x4>(res + pc[i].at * size);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) wt[i].load(a.weight, a.wdt, pc[i].at);
+    char *sum = a.sum.p[r] ? a.sum.p[r] + row * a.sum.pitch : nullptr;
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (RES) {
+            float t[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) t[e] = value<V, DT>(s[i], e) + value<V, DT>(q[i], e);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[i][e] = DT == kF32 ? __float_as_uint(t[e]) : pack_bf16(t[2 * e], t[2 * e + 1]);
+        }
+        float t = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) t = __builtin_fmaf(value<V, DT>(s[i], e), value<V, DT>(s[i], e), t);
+        if (pc[i].skip) {
+            t = 0.0f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float v = value<V, DT>(s[i], e);
+                t = e >= (int)pc[i].skip ? __builtin_fmaf(v, v, t) : t;
+            }
+        }
+        ss += t;
+    }
+    ss = team_all<OpSum>(ss, lds, &turn, waves);
+    // Stores only past the barrier: the sum or y may lie where x or the residual
+    // did, and the row's last vector shares elements with one of another wave.
+    if (sum) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (owned<V>(pc[i])) st_vec<NT>(sum + pc[i].at * size, s[i]);
+    }
+    const float rho = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, a.inv_width, a.eps));
+    float y[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float w[V];
+        wt[i].values(a.weight, a.wdt, w);
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[i][e] = value<V, DT>(s[i], e) * rho * w[e];
+    }
+    char *out = a.y.p[r] + row * a.y.pitch;
+    if constexpr (k8) {
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) most = OpMaxAbs::of(most, fabsf(y[i][e]));
+        most = team_all<OpMaxAbs>(most, lds, &turn, waves);
+        const Quant qt = quant_of<YT>(most);
+        if (threadIdx.x == 0) st_elem<float>(a.scale.p[r], row, qt.scale);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!owned<V>(pc[i])) continue;
+            if constexpr (V == 8)
+                st_vec<NT>(out + pc[i].at, u32x2{codes_of<YT>(&y[i][0], qt), codes_of<YT>(&y[i][4], qt)});
+            else
+                st_vec<NT>(out + pc[i].at, codes_of<YT>(&y[i][0], qt));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (owned<V>(pc[i])) st_values<V, YT, NT>(out + pc[i].at * kSize<YT>, y[i]);
+    }
+}
+
 // ---------------------------------------------------------------- backward
 
 struct NormGradArgs {
     RowPtrs s, dy, dsum, dx;
     int64_t rows[DDP_MAX_RANKS];
     const char *weight;
-    float *part;        // [n_ranks][blocks][width] partial weight gradients, or null
-    int64_t width;
+    float *part;        // [n_ranks][blocks][part_width] partial weight gradients, or null
+    int64_t width, part_width;   // part_width: width up to a multiple of 8
     int wdt;
-    float eps;
+    float eps, inv_width;
 };
 
 template <int DT, int YT>
@@ -130,7 +298,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_rows(NormGradArgs a)
     constexpr int waves = kNormThreads / kWave;
     const int r = blockIdx.y;
     const int64_t W = a.width;
-    float *part = a.part ? a.part + ((int64_t)r * gridDim.x + blockIdx.x) * W : nullptr;
+    float *part = a.part ? a.part + ((int64_t)r * gridDim.x + blockIdx.x) * a.part_width : nullptr;
     if (part)
         for (int64_t j = threadIdx.x; j < W; j += kNormThreads) part[j] = 0.0f;
     for (int64_t row = blockIdx.x; row < a.rows[r]; row += gridDim.x) {
@@ -160,22 +328,151 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_rows(NormGradArgs a)
     }
 }
 
+// The backward with the row in registers, as norm_held, a block stepping through
+// a stretch of its rank's rows, with the next row's loads issued before this
+// row's sums are exchanged (PF; without it where the registers would not hold
+// two rows).  Each thread keeps the weight gradient of its own vectors in
+// registers over all the rows of its block; they are written in the vectors'
+// order (norm_grad_weight finds a column's place).
+template <int DT, int YT, int NV, bool PF, bool NT>
+__global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArgs a)
+{
+    constexpr int V = kVec<DT>, size = kSize<DT>, ysize = kSize<YT>;
+    using Dy = Raw<V, YT>;
+    __shared__ float lds[4 * kMostWaves];
+    int turn = 0;
+    const int r = blockIdx.y, threads = blockDim.x, waves = threads / kWave;
+    const int64_t rows = a.rows[r];
+    const bool has_q = a.dsum.p[r] != nullptr;
+    Piece pc[NV];
+    float w[NV][V], acc[NV][V];
+    u32x4 s[NV], q[NV];
+    Dy d[NV];
+    Weight<V> wt[NV];
+    // this block's rows: a stretch of its rank's
+    const int64_t per = (rows + gridDim.x - 1) / gridDim.x;
+    const int64_t end = min(rows, (blockIdx.x + 1) * per);
+    int64_t row = blockIdx.x * per;
+    auto fetch = [&](int64_t at_row) {
+        const char *sp = a.s.p[r] + at_row * a.s.pitch, *dp = a.dy.p[r] + at_row * a.dy.pitch;
+        const char *qp = a.dsum.p[r] + at_row * a.dsum.pitch;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            s[i] = ld_vec<NT, u32x4>(sp + pc[i].at * size);
+            d[i] = ld_vec<NT, Dy>(dp + pc[i].at * ysize);
+            if (has_q) q[i] = ld_vec<NT, u32x4>(qp + pc[i].at * size);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        pc[i] = piece_of<V>(i * threads + (int)threadIdx.x, (int)a.width);
+        wt[i].load(a.weight, a.wdt, pc[i].at);
+        q[i] = u32x4{0, 0, 0, 0};
+    }
+    if (PF && row < end) fetch(row);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        wt[i].values(a.weight, a.wdt, w[i]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[i][e] = 0.0f;
+    }
+    for (; row < end; ++row) {
+        if (!PF) fetch(row);
+        u32x4 s0[NV], q0[NV];
+        Dy d0[NV];
+        float ss = 0.0f, gs = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            s0[i] = s[i];
+            d0[i] = d[i];
+            q0[i] = q[i];
+            float t = 0.0f, u = 0.0f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float v = value<V, DT>(s0[i], e);
+                t = __builtin_fmaf(v, v, t);
+                u = __builtin_fmaf(value<V, YT>(d0[i], e) * w[i][e], v, u);
+            }
+            if (pc[i].skip) {
+                t = u = 0.0f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float v = value<V, DT>(s0[i], e);
+                    const bool mine = e >= (int)pc[i].skip;
+                    t = mine ? __builtin_fmaf(v, v, t) : t;
+                    u = mine ? __builtin_fmaf(value<V, YT>(d0[i], e) * w[i][e], v, u) : u;
+                }
+            }
+            ss += t;
+            gs += u;
+        }
+        if (PF && row + 1 < end) fetch(row + 1);
+        ss = wave_all<OpSum>(ss);
+        gs = wave_all<OpSum>(gs);
+        if (waves > 1) {
+            float *slot = lds + turn * 2 * kMostWaves;
+            turn ^= 1;
+            if (threadIdx.x % kWave == 0) {
+                slot[threadIdx.x / kWave] = ss;
+                slot[kMostWaves + threadIdx.x / kWave] = gs;
+            }
+            __syncthreads();
+            ss = join_waves<OpSum>(slot, waves, 0.0f);
+            gs = join_waves<OpSum>(slot + kMostWaves, waves, 0.0f);
+        }
+        const float rho = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, a.inv_width, a.eps));
+        const float c = rho * rho * (gs * a.inv_width);
+        char *dx = a.dx.p[r] + row * a.dx.pitch;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float o[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float v = value<V, DT>(s0[i], e), g = value<V, YT>(d0[i], e);
+                o[e] = rho * (g * w[i][e] - v * c);
+                if (has_q) o[e] = value<V, DT>(q0[i], e) + o[e];
+                acc[i][e] = __builtin_fmaf(g, v * rho, acc[i][e]);
+            }
+            if (owned<V>(pc[i])) st_values<V, DT, NT>(dx + pc[i].at * size, o);
+        }
+    }
+    if (!a.part) return;
+    char *part = reinterpret_cast<char *>(a.part + ((int64_t)r * gridDim.x + blockIdx.x) * a.part_width);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (owned<V>(pc[i]))
+            st_values<V, kF32, false>(part + (int64_t)(i * threads + (int)threadIdx.x) * V * 4, acc[i]);
+}
+
+// The weight gradients: a block sums 64 columns of one rank's partial sums,
+// each of its waves a stretch of the blocks, joined in the waves' order.
 struct DwArgs {
     VecPtrs dw;
-    int64_t width;
-    int64_t parts;
+    int64_t width, part_width;
+    int64_t last, shift;    // columns from `last` on lie `shift` further (a row's last vector)
+    int32_t parts;
     const float *part;
     int dt, accumulate;
 };
 
-__global__ void __launch_bounds__(kNormThreads) norm_grad_weight(DwArgs a, int64_t first_block)
+constexpr int kDwWaves = 8;
+
+__global__ void __launch_bounds__(kDwWaves * kWave) norm_grad_weight(DwArgs a, int64_t first_block)
 {
-    const int r = blockIdx.y;
-    const int64_t j = (first_block + blockIdx.x) * kNormThreads + threadIdx.x;
-    if (j >= a.width) return;
-    const float *p = a.part + (int64_t)r * a.parts * a.width + j;
+    __shared__ float lds[kDwWaves][kWave];
+    const int r = blockIdx.y, wave = threadIdx.x / kWave, l = threadIdx.x % kWave;
+    const int64_t j = (first_block + blockIdx.x) * kWave + l;
+    const float *p = a.part + (int64_t)r * a.parts * a.part_width +
+                     (j < a.last ? j : j < a.width ? j + a.shift : 0);
+    const int per = (a.parts + kDwWaves - 1) / kDwWaves;
+    const int b0 = wave * per, b1 = min(b0 + per, a.parts);
     float t = 0.0f;
-    for (int64_t b = 0; b < a.parts; ++b) t += p[b * a.width];
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) t += p[b * a.part_width];
+    lds[wave][l] = t;
+    __syncthreads();
+    if (wave || j >= a.width) return;
+    for (int k = 1; k < kDwWaves; ++k) t += lds[k][l];
     char *dw = a.dw.p[r];
     if (a.dt == kF32)
         store_elem<kF32>(dw, j, a.accumulate ? load_elem<kF32>(dw, j) + t : t);
@@ -183,28 +480,114 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_weight(DwArgs a, int64
         store_elem<kBF16>(dw, j, a.accumulate ? load_elem<kBF16>(dw, j) + t : t);
 }
 
-// Blocks of each rank in the backward, each with its own partial weight
-// gradient.
-int64_t grad_blocks(int64_t most, int32_t n_ranks)
-{
-    return std::max<int64_t>(1, std::min<int64_t>(most, std::max(1, 512 / n_ranks)));
-}
+int64_t padded(int64_t width) { return (width + 7) / 8 * 8; }
 
 int dtype_bytes(int dt) { return dt == DDP_F32 ? 4 : dt == DDP_BF16 ? 2 : 1; }
 bool eight(int dt) { return dt == DDP_I8 || dt == DDP_E4M3; }
 
 bool eps_ok(float eps) { return eps >= 0.0f && std::isfinite(eps); }
 
-template <int DT, int YT>
-void launch_norm(const NormArgs &a, bool res, dim3 g, hipStream_t st)
+// The kernel for rows of `width` elements, `vec` to a 16-byte vector: the
+// vectors each thread of a block holds, as few as let a block of at most 16
+// waves hold the row (more, smaller shares per thread measured as fast or
+// faster: 8 x 2048 x 4096 bf16 forward 87.0 us with 1, 87.2 us with 2), or 0
+// where no block can and the row is read from memory in every pass.
+constexpr int64_t kMostThreads = kMostWaves * kWave;
+int held_vectors(int64_t width, int64_t vec, int most)
 {
-    if (res)
-        norm_rows<DT, YT, true><<<g, kNormThreads, 0, st>>>(a);
-    else
-        norm_rows<DT, YT, false><<<g, kNormThreads, 0, st>>>(a);
+    const int64_t vecs = (width + vec - 1) / vec;
+    if (width < vec || vecs > most * kMostThreads) return 0;
+    return vecs <= kMostThreads ? 1 : vecs <= 2 * kMostThreads ? 2 : 4;
+}
+int held_threads(int64_t width, int64_t vec, int nv)
+{
+    return (int)(((width + vec - 1) / vec + nv * kWave - 1) / (nv * kWave)) * kWave;
+}
+// What the backward holds per thread: four vectors only where they are f32 (a
+// thread's weights and weight gradient take two registers an element: with
+// bf16's eight to a vector the row would spill).
+int grad_held_vectors(int64_t width, int64_t vec) { return held_vectors(width, vec, vec == 4 ? 4 : 2); }
+
+// Blocks of each rank in the backward, each with its own partial weight
+// gradient: eight waves, and one block at least, to each of the 256 CUs.  Two
+// tensors in and one out per row are in flight twice over (the prefetch), so
+// more waves bring no bandwidth and cost partial sums: 8 x 2048 x 4096 bf16
+// takes 97 us with 2048 waves in all, 136 with 1024, 103 with 4096 and 113
+// with 8192; 4096 x 8192 f32 (16 waves to a block) 102 us with 256 blocks and
+// 111 with 128.
+constexpr int64_t kCus = 256, kWavesPerCu = 8;
+int64_t grad_blocks(int64_t most, int32_t n_ranks, int64_t width, int64_t vec)
+{
+    const int nv = grad_held_vectors(width, vec);
+    const int64_t waves = nv ? held_threads(width, vec, nv) / kWave : kNormThreads / kWave;
+    int64_t blocks = kCus * std::max<int64_t>(1, kWavesPerCu / waves);
+    // rows too wide for registers: at most 64 MB of partial sums
+    if (!nv) blocks = std::min(blocks, std::max<int64_t>(8, ((int64_t)16 << 20) / width));
+    return std::max<int64_t>(1, std::min(most, blocks / n_ranks));
 }
 
-constexpr int64_t kMostGridRows = 1 << 16;   // rows of a grid; blocks step through the rest
+template <int DT, int YT, bool RES, bool NT>
+ddp_status_t launch_norm_as(const NormArgs &a, int64_t most, int32_t n_ranks, hipStream_t st)
+{
+    constexpr int V = kVec<DT>;
+    const int nv = held_vectors(a.width, V, 4);
+    if (!nv) {
+        const dim3 g((unsigned)std::min(most, kMostGridRows), (unsigned)n_ranks);
+        norm_rows<DT, YT, RES><<<g, kNormThreads, 0, st>>>(a);
+        return launched("norm kernel launch");
+    }
+    const int threads = held_threads(a.width, V, nv);
+    return launch_split(most, threads, "norm kernel launch", [&](int64_t b0, unsigned nb) {
+        const dim3 g(nb, (unsigned)n_ranks);
+        if (nv == 1)
+            norm_held<DT, YT, RES, 1, NT><<<g, threads, 0, st>>>(a, b0);
+        else if (nv == 2)
+            norm_held<DT, YT, RES, 2, NT><<<g, threads, 0, st>>>(a, b0);
+        else
+            norm_held<DT, YT, RES, 4, NT><<<g, threads, 0, st>>>(a, b0);
+    });
+}
+
+template <int DT, int YT, bool NT>
+void launch_grad_as(const NormGradArgs &a, dim3 g, hipStream_t st)
+{
+    constexpr int V = kVec<DT>;
+    const int nv = grad_held_vectors(a.width, V);
+    const int threads = nv ? held_threads(a.width, V, nv) : kNormThreads;
+    if (nv == 1)
+        norm_grad_held<DT, YT, 1, true, NT><<<g, threads, 0, st>>>(a);
+    else if (nv == 2)
+        norm_grad_held<DT, YT, 2, true, NT><<<g, threads, 0, st>>>(a);
+    else if (nv == 4) {
+        if constexpr (DT == kF32) norm_grad_held<DT, YT, 4, false, NT><<<g, threads, 0, st>>>(a);
+    } else
+        norm_grad_rows<DT, YT><<<g, threads, 0, st>>>(a);
+}
+
+// Bytes moved from which a call's accesses are non-temporal: what no longer
+// fits the 256 MB last-level cache.  8 x 2048 x 4096 bf16 (537 MB) takes 87 us
+// with nt and 94 without, the backward 97 and 107; 4 x 1021 x 4096 to 8 bits
+// (117 MB) with its read-back 73 us without and 78 with, since the next reader
+// finds the codes in the cache.
+constexpr int64_t kStreamBytes = (int64_t)256 << 20;
+
+template <int DT, int YT>
+ddp_status_t launch_norm(const NormArgs &a, bool res, bool nt, int64_t most, int32_t n, hipStream_t st)
+{
+    if (res)
+        return nt ? launch_norm_as<DT, YT, true, true>(a, most, n, st)
+                  : launch_norm_as<DT, YT, true, false>(a, most, n, st);
+    return nt ? launch_norm_as<DT, YT, false, true>(a, most, n, st)
+              : launch_norm_as<DT, YT, false, false>(a, most, n, st);
+}
+
+template <int DT, int YT>
+void launch_grad(const NormGradArgs &a, bool nt, dim3 g, hipStream_t st)
+{
+    if (nt) launch_grad_as<DT, YT, true>(a, g, st);
+    else launch_grad_as<DT, YT, false>(a, g, st);
+}
+
 
 }  // namespace
 
@@ -250,27 +633,28 @@ ddp_status_t ddp_rms_norm(const int64_t *rows, int32_t n_ranks, int64_t width, c
     a.wdt = weight_dtype;
     a.width = width;
     a.eps = eps;
-    const dim3 g((unsigned)std::min(most, kMostGridRows), (unsigned)n_ranks);
+    a.inv_width = 1.0f / (float)width;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const bool res = residual != nullptr;
+    const bool nt = total * width * (esz * (1 + (res ? 1 : 0) + (sum_out ? 1 : 0)) + ysz) >= kStreamBytes;
     if (dtype == DDP_F32) {
-        if (y_dtype == DDP_F32) launch_norm<kF32, kF32>(a, res, g, hs);
-        else if (y_dtype == DDP_BF16) launch_norm<kF32, kBF16>(a, res, g, hs);
-        else if (y_dtype == DDP_I8) launch_norm<kF32, kI8>(a, res, g, hs);
-        else launch_norm<kF32, kE4M3>(a, res, g, hs);
-    } else {
-        if (y_dtype == DDP_BF16) launch_norm<kBF16, kBF16>(a, res, g, hs);
-        else if (y_dtype == DDP_I8) launch_norm<kBF16, kI8>(a, res, g, hs);
-        else launch_norm<kBF16, kE4M3>(a, res, g, hs);
+        if (y_dtype == DDP_F32) return launch_norm<kF32, kF32>(a, res, nt, most, n_ranks, hs);
+        if (y_dtype == DDP_BF16) return launch_norm<kF32, kBF16>(a, res, nt, most, n_ranks, hs);
+        if (y_dtype == DDP_I8) return launch_norm<kF32, kI8>(a, res, nt, most, n_ranks, hs);
+        return launch_norm<kF32, kE4M3>(a, res, nt, most, n_ranks, hs);
     }
-    return launched("norm kernel launch");
+    if (y_dtype == DDP_BF16) return launch_norm<kBF16, kBF16>(a, res, nt, most, n_ranks, hs);
+    if (y_dtype == DDP_I8) return launch_norm<kBF16, kI8>(a, res, nt, most, n_ranks, hs);
+    return launch_norm<kBF16, kE4M3>(a, res, nt, most, n_ranks, hs);
 }
 
 int64_t ddp_rms_norm_grad_workspace(const int64_t *rows, int32_t n_ranks, int64_t width)
 {
     int64_t total, most;
     if (check_shape(rows, n_ranks, width, &total, &most) != DDP_OK) return -1;
-    return (int64_t)sizeof(float) * n_ranks * grad_blocks(most, n_ranks) * width;
+    // either dtype's number of blocks
+    const int64_t blocks = std::max(grad_blocks(most, n_ranks, width, 4), grad_blocks(most, n_ranks, width, 8));
+    return (int64_t)sizeof(float) * n_ranks * blocks * padded(width);
 }
 
 ddp_status_t ddp_rms_norm_grad(const int64_t *rows, int32_t n_ranks, int64_t width,
@@ -292,7 +676,8 @@ ddp_status_t ddp_rms_norm_grad(const int64_t *rows, int32_t n_ranks, int64_t wid
                       (dsum && !dsum->rank)))
         return DDP_ERR_INVALID_ARG;
     const int esz = dtype_size(dtype), ysz = dtype_size(dy_dtype);
-    const int64_t blocks = grad_blocks(most, n_ranks);
+    const int64_t vec = vec_elems(dtype);
+    const int64_t blocks = grad_blocks(most, n_ranks, width, vec);
     const int64_t need = ddp_rms_norm_grad_workspace(rows, n_ranks, width);
     if (dweight) {
         if (!workspace || !aligned(workspace, 16)) return DDP_ERR_INVALID_ARG;
@@ -324,26 +709,36 @@ ddp_status_t ddp_rms_norm_grad(const int64_t *rows, int32_t n_ranks, int64_t wid
     a.wdt = weight_dtype;
     a.part = dweight ? static_cast<float *>(workspace) : nullptr;
     a.width = width;
+    a.part_width = padded(width);
     a.eps = eps;
+    a.inv_width = 1.0f / (float)width;
+    const bool nt = total * width * (esz * (2 + (dsum ? 1 : 0)) + ysz) >= kStreamBytes;
     const dim3 g((unsigned)blocks, (unsigned)n_ranks);
     if (dtype == DDP_BF16)
-        norm_grad_rows<kBF16, kBF16><<<g, kNormThreads, 0, hs>>>(a);
+        launch_grad<kBF16, kBF16>(a, nt, g, hs);
     else if (dy_dtype == DDP_F32)
-        norm_grad_rows<kF32, kF32><<<g, kNormThreads, 0, hs>>>(a);
+        launch_grad<kF32, kF32>(a, nt, g, hs);
     else
-        norm_grad_rows<kF32, kBF16><<<g, kNormThreads, 0, hs>>>(a);
+        launch_grad<kF32, kBF16>(a, nt, g, hs);
     if ((st = launched("norm gradient kernel launch")) != DDP_OK || !dweight) return st;
     DwArgs w;
     std::memset(&w, 0, sizeof(w));
     set_vecs(&w.dw, dweight, n_ranks);
     w.width = width;
-    w.parts = blocks;
+    w.part_width = a.part_width;
+    w.last = width;
+    if (grad_held_vectors(width, vec)) {
+        const int64_t vecs = (width + vec - 1) / vec;
+        w.last = (vecs - 1) * vec;
+        w.shift = vecs * vec - width;
+    }
+    w.parts = (int32_t)blocks;
     w.part = a.part;
     w.dt = dweight_dtype;
     w.accumulate = accumulate != 0;
-    return launch_split((width + kNormThreads - 1) / kNormThreads, kNormThreads,
+    return launch_split((width + kWave - 1) / kWave, kDwWaves * kWave,
                         "weight gradient kernel launch", [&](int64_t b0, unsigned nb) {
-                            norm_grad_weight<<<dim3(nb, (unsigned)n_ranks), kNormThreads, 0, hs>>>(w, b0);
+                            norm_grad_weight<<<dim3(nb, (unsigned)n_ranks), kDwWaves * kWave, 0, hs>>>(w, b0);
                         });
 }
 

@@ -3,6 +3,8 @@
 // of the ABI.
 #pragma once
 
+#include <type_traits>
+
 #include "device.h"
 
 namespace ddp_detail {
@@ -46,14 +48,30 @@ struct OpMax {
     static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
 };
 
-// Every lane gets the whole wave's value; the tree is the same for each lane,
-// and the operations commute, so all lanes hold the same bits.
+// Every lane gets the whole wave's value.  Six steps on the vector ALU, no
+// LDS: pairs and quads by quad_perm, then the halves of 8 and 16 lanes mirrored
+// (each half already holds one value in all its lanes), then rows of 16 and
+// halves of 32 exchanged.  The operations commute, so all lanes hold the same
+// bits.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x)
+{
+    const int v = __float_as_int(x);
+    return __int_as_float(__builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false));
+}
 template <class Op>
 __device__ __forceinline__ float wave_all(float x)
 {
-#pragma unroll
-    for (int d = kWave / 2; d > 0; d >>= 1) x = Op::of(x, __shfl_xor(x, d, kWave));
-    return x;
+    x = Op::of(x, dpp<0xB1>(x));    // quad_perm [1, 0, 3, 2]
+    x = Op::of(x, dpp<0x4E>(x));    // quad_perm [2, 3, 0, 1]
+    x = Op::of(x, dpp<0x141>(x));   // row_half_mirror
+    x = Op::of(x, dpp<0x140>(x));   // row_mirror
+    const uint32_t u = __float_as_uint(x);
+    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    x = Op::of(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    const uint32_t w = __float_as_uint(x);
+    r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    return Op::of(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 // Every thread of a block of `waves` waves gets the block's value.  `lds`
@@ -71,9 +89,121 @@ __device__ __forceinline__ float block_all(float x, float *lds, int waves)
     return y;
 }
 
+// One value of each wave of a block, joined: `slot` holds the waves' values (at
+// most 16).  Every lane reads one of them (`none` past the last wave) and rows
+// of 16 lanes join theirs by dpp, so one LDS read is waited for, not one per
+// wave.
+constexpr int kMostWaves = 16;
+template <class Op>
+__device__ __forceinline__ float join_waves(const float *slot, int waves, float none)
+{
+    const int l = threadIdx.x % kMostWaves;
+    float x = l < waves ? slot[l] : none;
+    x = Op::of(x, dpp<0xB1>(x));
+    x = Op::of(x, dpp<0x4E>(x));
+    x = Op::of(x, dpp<0x141>(x));
+    return Op::of(x, dpp<0x140>(x));
+}
+
+// block_all with one barrier: `lds` holds 2 * 16 floats and `turn` alternates
+// between consecutive calls, so a slot is written again only after a barrier
+// that every wave reaches past its reads.
+template <class Op>
+__device__ __forceinline__ float team_all(float x, float *lds, int *turn, int waves, float none = 0.0f)
+{
+    x = wave_all<Op>(x);
+    if (waves == 1) return x;
+    float *slot = lds + *turn * kMostWaves;
+    *turn ^= 1;
+    if (threadIdx.x % kWave == 0) slot[threadIdx.x / kWave] = x;
+    __syncthreads();
+    return join_waves<Op>(slot, waves, none);
+}
+
 __device__ __forceinline__ float load_as(const char *p, int64_t i, int dt)
 {
     return dt == kF32 ? ld_elem<float>(p, i) : widen_bf16(ld_elem<uint16_t>(p, i));
+}
+
+
+// ---------------------------------------------------------------- vectors
+// A lane's piece of a row: 16 bytes of f32 or bf16, at any element alignment.
+template <int DT> constexpr int kVec = DT == kF32 ? 4 : 8;
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Two floats rounded to bf16 (nearest, ties to even; a NaN stays one) in one
+// instruction.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
+template <bool NT, class V>
+__device__ __forceinline__ V ld_vec(const char *p)
+{
+    typedef V VU __attribute__((aligned(1)));
+    if (NT) return __builtin_nontemporal_load(reinterpret_cast<const VU *>(p));
+    return *reinterpret_cast<const VU *>(p);
+}
+template <bool NT, class V>
+__device__ __forceinline__ void st_vec(char *p, const V &v)
+{
+    typedef V VU __attribute__((aligned(1)));
+    if (NT)
+        __builtin_nontemporal_store(static_cast<VU>(v), reinterpret_cast<VU *>(p));
+    else
+        *reinterpret_cast<VU *>(p) = v;
+}
+
+// A row of n >= V elements as vectors of V: vector k covers [k * V, k * V + V),
+// but for the last one, which ends with the row and so may share elements with
+// the one before.  Both hold (and store) the same values there; sums count an
+// element once, for the vector that starts at or before k * V.  So no row end
+// takes a path by element.
+struct Piece {
+    uint32_t at;      // first element
+    uint32_t skip;    // elements of it that another vector counts: 0 but for the last vector,
+                      // V or more past the end
+};
+template <int V>
+__device__ __forceinline__ Piece piece_of(int k, int n)
+{
+    const int j = k * V, at = min(j, n - V);
+    return {(uint32_t)at, (uint32_t)(j - at)};
+}
+template <int V>
+__device__ __forceinline__ bool owned(const Piece &p) { return p.skip < V; }
+
+template <int DT> constexpr int kSize = DT == kF32 ? 4 : 2;
+
+// V values as a vector of OUT elements at p.
+template <int V, int OUT, bool NT>
+__device__ __forceinline__ void st_values(char *p, const float *y)
+{
+    if constexpr (OUT == kF32) {
+#pragma unroll
+        for (int h = 0; h < V / 4; ++h)
+            st_vec<NT>(p + 16 * h,
+                       u32x4{__float_as_uint(y[4 * h]), __float_as_uint(y[4 * h + 1]),
+                             __float_as_uint(y[4 * h + 2]), __float_as_uint(y[4 * h + 3])});
+    } else if constexpr (V == 8) {
+        st_vec<NT>(p, u32x4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                            pack_bf16(y[6], y[7])});
+    } else {
+        st_vec<NT>(p, u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])});
+    }
+}
+
+// V elements of DT, raw and as floats.
+template <int V, int DT>
+using Raw = std::conditional_t<V * kSize<DT> == 16, u32x4, u32x2>;
+template <int V, int DT>
+__device__ __forceinline__ float value(const Raw<V, DT> &v, int e)
+{
+    if (DT == kF32) return __uint_as_float(v[e]);
+    return __uint_as_float((e & 1) ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16);
 }
 
 }  // namespace ddp_detail

@@ -135,9 +135,10 @@ def test_more_rows_than_a_grid(ddp):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("width", [5, 2048, 5003, 40009])
+@pytest.mark.parametrize("width", [5, 257, 513, 2048, 2051, 4097, 5003, 8195, 8200, 40009])
 def test_in_place(ddp, dtype, width):
-    rows = 6
+    """Among the widths those whose last, partial vector is the first of a wave."""
+    rows = 600
     x0, r0 = _rand(0, rows, width, dtype).cuda(), _rand(1, rows, width, dtype).cuda()
     w = _weight(0, width, dtype)
     s0 = norm_sum(x0, r0)

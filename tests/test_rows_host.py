@@ -16,12 +16,18 @@ def _rows(*n):
     return (ctypes.c_int64 * len(n))(*n)
 
 
+class _RowsC(ctypes.Structure):
+    """ddp_rows_t."""
+    _fields_ = [("rank", ctypes.c_void_p), ("stride", ctypes.c_int64)]
+
+
 class Matrix:
     """A ddp_rows_t over made-up addresses."""
 
     def __init__(self, stride, *addr):
         self.arr = (ctypes.c_void_p * len(addr))(*addr)
-        self.c = ddp._RowsC(ctypes.addressof(self.arr), stride)
+        self.rows = _RowsC(ctypes.addressof(self.arr), stride)
+        self.c = ctypes.addressof(self.rows)
 
 
 def _vec(*addr):
@@ -159,6 +165,9 @@ def test_distill_refuses(g):
     assert f(ib=2) == INVALID
     for tau in (0.0, -1.0, math.nan, math.inf):
         assert f(tau=tau) == INVALID
+    for tau in (9e-7, 2e6):
+        assert f(tau=tau) == UNSUPPORTED
+    assert f(vocab=1 << 31, z=(1 << 31, 1 << 40, 1 << 50), dz=(1 << 31, 1 << 41, 1 << 51)) == UNSUPPORTED
     assert f(loss=None) == INVALID
     assert f(loss=9 * MB + 2) == INVALID
     for k in ("z", "t", "i"):

@@ -1,8 +1,30 @@
 // Distillation from a teacher's top logits, forward and backward
 // (ddp_distill_loss, ddp_distill_grad).
+//
+//     p = softmax(t / tau) over a token's live entries;  q = softmax(z / tau)
+//     row = tau^2 sum_k p_k (log p_k - log q_{i_k})
+//         = tau^2 (sum_k p_k (log p_k - (z_{i_k} - r) / tau) + (m - r) / tau + log s)
+//     dz_j = c (q_j - sum_{k: i_k = j} p_k),   c = grad_scale N tau w / D
+// with m the largest logit, s = sum of exp((z - m) / tau) and any r, as the p
+// add up to 1.  The teacher's part is a few entries; what costs is reading the
+// logits once and writing the gradient once, 2 + 2 bytes and one exp per
+// logit in bf16: HBM bounds it.
+//
+// A thread's exponentials are taken against its own largest logit, as soon as
+// its logits arrive, and one exchange of (m, s) pairs joins them:
+// exp((z - m) / tau) = exp((z - m_own) / tau) exp((m_own - m) / tau).  So each
+// logit has one exp and nothing waits for the row's largest before that.
+//
+// Three kernels, chosen by the vocabulary and the number of tokens:
+//   distill_held   a block to a token, the row's exponentials in registers;
+//   distill_far    a block to a token, the row read twice: vocabularies that
+//                  registers do not hold (or shorter than a vector);
+//   distill_part,  few tokens: several blocks to a token, joined through the
+//   distill_emit   workspace, the second pass over rows the caches still hold.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -14,32 +36,60 @@ using namespace ddp_detail;
 
 namespace {
 
-constexpr int kDistillThreads = 256;
+constexpr int kFarThreads = 1024;     // distill_far, and the last sum of the loss
+constexpr int kPartThreads = 256;     // distill_part, distill_emit
+constexpr int kLiveThreads = 256;     // distill_live
+constexpr int kMostLiveBlocks = 256;  // of all ranks together
+constexpr int kMostSplits = 64;       // blocks to a token
+constexpr float kLn2 = 0.69314718f;
 
 struct DistillArgs {
     RowPtrs z, teacher, index, dz;
     VecPtrs weight, row_loss;
     int64_t rows[DDP_MAX_RANKS];
     int64_t first[DDP_MAX_RANKS];   // tokens of the ranks before
+    int64_t tokens;
     int64_t vocab;
-    int32_t n_ranks, top;
+    int64_t seg;                    // logits of a split (distill_part, distill_emit)
+    int32_t n_ranks, top, splits;
     int tdt, index_bytes;
     float tau, scale;               // scale: grad_scale * n_ranks * tau
-    float *den;                     // D
+    float inv_tau, exp_scale;       // 1 / tau, log2(e) / tau
+    float far;                      // logits up to this times exp_scale are finite
+    int32_t live_blocks;            // parts of `den`
+    float *den;                     // [live_blocks] parts of D
     float *w;                       // [tokens] the weight of each live token, 0 for others
-    float *loss_of;                 // [tokens] row_loss
+    float *loss_of;                 // [tokens] row_loss; split rows: its part without m and s
+    float *ref;                     // [tokens] split rows: r
+    float *part;                    // [tokens][splits] pairs (m, s)
     float *loss;
 };
 
-// The vocabulary index of a token's entry k, or -1 where the entry is not
-// live, and its logit.
-__device__ __forceinline__ int64_t entry_of(const DistillArgs &a, int r, int64_t row, int k, float *t)
+// The teacher's entries of one token, in dynamic LDS: `padded` (top up to a
+// multiple of 4) of each.
+struct Entries {
+    int padded;
+    int32_t *at;     // the entry's place, -1 where it is not live or past the last
+    float *prob;     // p, 0 where it is not live
+    float *z;        // the student's logit there
+};
+__host__ __device__ inline int padded_top(int top) { return (top + 3) / 4 * 4; }
+__device__ __forceinline__ Entries entries_of(const DistillArgs &a)
 {
-    const char *ip = a.index.p[r] + row * a.index.pitch;
-    const int64_t j = a.index_bytes == 4 ? (int64_t)ld_elem<int32_t>(ip, k) : ld_elem<int64_t>(ip, k);
-    if (j < 0 || j >= a.vocab) return -1;
-    *t = load_as(a.teacher.p[r] + row * a.teacher.pitch, k, a.tdt);
-    return *t == -INFINITY ? -1 : j;
+    extern __shared__ __align__(16) int32_t entry_words[];
+    const int n = padded_top(a.top);
+    return {n, entry_words, reinterpret_cast<float *>(entry_words + n),
+            reinterpret_cast<float *>(entry_words + 2 * n)};
+}
+inline unsigned entry_bytes(int top) { return (unsigned)padded_top(top) * 12u; }
+
+// The row of a block.  Blocks go to the 8 XCDs in turn, so among each 8 rows
+// block b takes the one b / 8 further on: rows masked at a fixed distance (a
+// multiple of 2, say) then spread over all XCDs instead of leaving some idle.
+__device__ __forceinline__ int64_t row_of_block(int64_t b, int64_t rows)
+{
+    const int64_t g = b / kXcds * kXcds;
+    return g + kXcds <= rows ? g + (b % kXcds + b / kXcds) % kXcds : b;
 }
 
 __device__ __forceinline__ float weight_of(const DistillArgs &a, int r, int64_t row)
@@ -49,125 +99,752 @@ __device__ __forceinline__ float weight_of(const DistillArgs &a, int r, int64_t 
     return w > 0.0f ? w : 0.0f;
 }
 
-// w of every token (one thread each): 0 unless the token is live.
-__global__ void __launch_bounds__(kDistillThreads) distill_weights(DistillArgs a)
+// Entry k's place in the vocabulary, or -1 where it is not live, and its logit.
+__device__ __forceinline__ int32_t entry_of(const DistillArgs &a, const char *index, const char *teacher,
+                                            uint32_t k, float *t)
 {
-    const int r = blockIdx.y;
-    for (int64_t row = (int64_t)blockIdx.x * kDistillThreads + threadIdx.x; row < a.rows[r];
-         row += (int64_t)gridDim.x * kDistillThreads) {
-        float w = weight_of(a, r, row);
-        if (w > 0.0f) {
-            bool live = false;
-            float t;
-            for (int k = 0; k < a.top && !live; ++k) live = entry_of(a, r, row, k, &t) >= 0;
-            if (!live) w = 0.0f;
+    const int64_t j = a.index_bytes == 4 ? (int64_t)ld_elem<int32_t>(index + k * 4u, 0)
+                                         : ld_elem<int64_t>(index + k * 8u, 0);
+    *t = a.tdt == kF32 ? ld_elem<float>(teacher + k * 4u, 0) : widen_bf16(ld_elem<uint16_t>(teacher + k * 2u, 0));
+    return j >= 0 && j < a.vocab && *t > -INFINITY ? (int32_t)j : -1;
+}
+
+__device__ __forceinline__ float exp_of(const DistillArgs &a, float below)
+{
+    return __builtin_amdgcn_exp2f(below * a.exp_scale);
+}
+
+// A lane's first entry (k = lane), loaded ahead of the logits, and the student's
+// logit there: raw words, so that nothing waits for a load before its value
+// is needed.
+struct FirstEntry {
+    uint32_t lo, hi, t, z;
+    __device__ __forceinline__ void load(const DistillArgs &a, int r, int64_t row)
+    {
+        const int k = min((int)(threadIdx.x % kWave), a.top - 1);
+        const char *index = a.index.p[r] + row * a.index.pitch + k * a.index_bytes;
+        const char *teacher = a.teacher.p[r] + row * a.teacher.pitch;
+        lo = ld_elem<uint32_t>(index, 0);
+        if (a.index_bytes == 8) hi = ld_elem<uint32_t>(index, 1);
+        if (a.tdt == kF32)
+            t = ld_elem<uint32_t>(teacher, k);
+        else
+            t = ld_elem<uint16_t>(teacher, k);
+    }
+    // The entry's place, -1 where it is not live.
+    __device__ __forceinline__ int32_t place(const DistillArgs &a) const
+    {
+        const int64_t j = a.index_bytes == 8 ? (int64_t)((uint64_t)hi << 32 | lo) : (int64_t)(int32_t)lo;
+        return (int)(threadIdx.x % kWave) < a.top && j >= 0 && j < a.vocab && logit(a) > -INFINITY ? (int32_t)j : -1;
+    }
+    __device__ __forceinline__ float logit(const DistillArgs &a) const
+    {
+        return __uint_as_float(a.tdt == kF32 ? t : t << 16);
+    }
+    template <int DT>
+    __device__ __forceinline__ void gather(const DistillArgs &a, const char *row_z, int64_t from, int64_t to)
+    {
+        int64_t j = place(a);
+        j = j >= from && j < to ? j : from;
+        z = DT == kF32 ? ld_elem<uint32_t>(row_z, j) : (uint32_t)ld_elem<uint16_t>(row_z, j);
+    }
+    template <int DT>
+    __device__ __forceinline__ float student() const
+    {
+        return __uint_as_float(DT == kF32 ? z : z << 16);
+    }
+};
+
+// One wave: the token's entries into LDS, p among them (each lane its own
+// entries k = lane, lane + 64, ...), and the student's logits there, those in
+// [lo, hi).  Returns whether one is live.
+template <int DT>
+__device__ __forceinline__ bool teacher_of(const DistillArgs &a, int r, int64_t row, const Entries &en,
+                                           const FirstEntry &first, const char *z, int64_t lo, int64_t hi)
+{
+    const int l = threadIdx.x % kWave;
+    const char *index = a.index.p[r] + row * a.index.pitch, *teacher = a.teacher.p[r] + row * a.teacher.pitch;
+    const int padded = en.padded;
+    const int32_t mine = first.place(a);
+    float tm = mine >= 0 ? first.logit(a) : -INFINITY;
+    if (l < padded) {
+        en.at[l] = mine;
+        en.prob[l] = first.logit(a);
+        en.z[l] = first.student<DT>();
+    }
+#pragma unroll 1
+    for (int k0 = kWave; k0 < padded; k0 += kWave) {
+        const int k = k0 + l;
+        if (k >= padded) break;
+        float t = 0.0f;
+        const int32_t j = k < a.top ? entry_of(a, index, teacher, k, &t) : -1;
+        en.at[k] = j;
+        en.prob[k] = t;
+        if (j >= 0) tm = fmaxf(tm, t);
+        en.z[k] = j >= lo && j < hi ? load_elem<DT>(z, j) : 0.0f;
+    }
+    tm = wave_all<OpMax>(tm);
+    float mass = 0.0f;
+#pragma unroll 1
+    for (int k = l; k < padded; k += kWave) {
+        const float e = en.at[k] >= 0 ? exp_of(a, en.prob[k] - tm) : 0.0f;
+        en.prob[k] = e;
+        mass += e;
+    }
+    mass = 1.0f / wave_all<OpSum>(mass);
+#pragma unroll 1
+    for (int k = l; k < padded; k += kWave)
+        if (en.at[k] >= 0) en.prob[k] *= mass;
+    return tm > -INFINITY;
+}
+
+// The same wave, with every logit gathered: *ref = r, the largest of the
+// student's logits at the entries, and what is returned is
+// sum_k p_k (log p_k - (z_{i_k} - r) / tau).  An entry with p = 0 adds nothing,
+// whatever its logit.
+__device__ __forceinline__ float divergence_of(const DistillArgs &a, const Entries &en, float *ref)
+{
+    const int l = threadIdx.x % kWave;
+    float m = -FLT_MAX;   // not -inf, so that a forbidden entry's z - r is -inf
+#pragma unroll 1
+    for (int k = l; k < a.top; k += kWave)
+        if (en.prob[k] > 0.0f) m = fmaxf(m, en.z[k]);
+    m = wave_all<OpMax>(m);
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int k = l; k < a.top; k += kWave) {
+        const float p = en.prob[k];
+        if (p > 0.0f || p != p) sum += p * (logf(p) - (en.z[k] - m) * a.inv_tau);
+    }
+    *ref = m;
+    return wave_all<OpSum>(sum);
+}
+
+// Pairs of the lanes of a wave, joined: every lane gets the wave's.
+template <bool FAST>
+__device__ __forceinline__ void wave_join(const DistillArgs &a, float *m, float *s)
+{
+    const float own = *m;
+    *m = wave_all<OpMax>(own);
+    *s = wave_all<OpSum>(*s * (FAST ? __builtin_amdgcn_exp2f(own - *m) : exp_of(a, own - *m)));
+}
+
+// Pairs of a block's waves, from LDS (at most 16 of each): by the largest first
+// members, the second ones scaled by exp(own - largest).
+template <class Exp>
+__device__ __forceinline__ void join_by(const float *ms, const float *ss, int waves, float *m, float *s, Exp &&ex)
+{
+    const int l = threadIdx.x % kMostWaves;
+    const float own = l < waves ? ms[l] : -FLT_MAX, part = l < waves ? ss[l] : 0.0f;
+    float x = own;
+    x = OpMax::of(x, dpp<0xB1>(x));
+    x = OpMax::of(x, dpp<0x4E>(x));
+    x = OpMax::of(x, dpp<0x141>(x));
+    x = OpMax::of(x, dpp<0x140>(x));
+    float y = part * ex(own - x);
+    y += dpp<0xB1>(y);
+    y += dpp<0x4E>(y);
+    y += dpp<0x141>(y);
+    *s = y + dpp<0x140>(y);
+    *m = x;
+}
+__device__ __forceinline__ void join_pairs(const DistillArgs &a, const float *ms, const float *ss, int waves,
+                                           float *m, float *s)
+{
+    join_by(ms, ss, waves, m, s, [&](float d) { return exp_of(a, d); });
+}
+__device__ __forceinline__ void join_centres(const float *ms, const float *ss, int waves, float *m, float *s)
+{
+    join_by(ms, ss, waves, m, s, [](float d) { return __builtin_amdgcn_exp2f(d); });
+}
+
+// D, from its parts: every lane of a wave gets it.
+__device__ __forceinline__ float total_weight(const DistillArgs &a)
+{
+    float d = 0.0f;
+#pragma unroll 1
+    for (uint32_t b = threadIdx.x % kWave; b < (uint32_t)a.live_blocks; b += kWave) d += a.den[b];
+    return wave_all<OpSum>(d);
+}
+
+// dz at the entries' places within [lo, hi): every thread its own entries.  An
+// entry of an index named several times has the sum of their p, in their
+// order, so all of them store the same value.
+template <int DT, class Exp>
+__device__ __forceinline__ void emit_entries(const DistillArgs &a, const Entries &en, char *dz, Exp &&exp_z,
+                                             float inv_s, float c, int64_t lo, int64_t hi)
+{
+    const int padded = en.padded;
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    for (int k = threadIdx.x; k < a.top; k += blockDim.x) {
+        const int32_t j = en.at[k];
+        if (j < lo || j >= hi) continue;
+        float p = 0.0f;
+        for (int i = 0; i < padded; i += 4) {
+            const i32x4 at = *reinterpret_cast<const i32x4 *>(&en.at[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (at[e] == j) p += en.prob[i + e];
         }
-        a.w[a.first[r] + row] = w;
+        store_elem<DT>(dz, j, c * (exp_z(en.z[k]) * inv_s - p));
     }
 }
 
-// den = sum of w; with the losses of the tokens also loss = sum of w * row_loss / den.
-__global__ void __launch_bounds__(kDistillThreads) distill_total(DistillArgs a, int64_t tokens,
-                                                                 int with_loss)
+// A token that is not live: its loss, and zeros for its gradient, by the
+// threads of its block (elements [lo, hi) of the row).
+template <int DT>
+__device__ void emit_zeros(char *dz, int64_t lo, int64_t hi)
 {
-    __shared__ float lds[kDistillThreads / kWave];
+    constexpr int V = kVec<DT>;
+    const int64_t vecs = (hi - lo) / V;
+    for (int64_t k = threadIdx.x; k < vecs; k += blockDim.x)
+        st_vec<true>(dz + (lo + k * V) * kSize<DT>, u32x4{0, 0, 0, 0});
+    for (int64_t j = lo + vecs * V + threadIdx.x; j < hi; j += blockDim.x) store_elem<DT>(dz, j, 0.0f);
+}
+
+__device__ __forceinline__ void note_row(const DistillArgs &a, int r, int64_t row, float w, float loss)
+{
+    a.w[a.first[r] + row] = w;
+    a.loss_of[a.first[r] + row] = loss;
+    if (a.row_loss.p[r]) st_elem<float>(a.row_loss.p[r], row, loss);
+}
+
+// ---------------------------------------------------------------- D
+
+// D in parts, one to a block: each wave takes tokens in turn, its lanes the
+// token's entries.  (The gradient needs D before the first row is written;
+// the loss alone takes it from the rows' own weights.)
+__global__ void __launch_bounds__(kLiveThreads) distill_live(DistillArgs a)
+{
+    __shared__ float lds[kLiveThreads / kWave];
+    const int r = blockIdx.y, l = threadIdx.x % kWave;
+    const int64_t step = (int64_t)gridDim.x * (kLiveThreads / kWave);
+    float d = 0.0f;
+    for (int64_t row = (int64_t)blockIdx.x * (kLiveThreads / kWave) + threadIdx.x / kWave; row < a.rows[r];
+         row += step) {
+        const float w = weight_of(a, r, row);
+        if (w == 0.0f) continue;
+        const char *index = a.index.p[r] + row * a.index.pitch;
+        const char *teacher = a.teacher.p[r] + row * a.teacher.pitch;
+        bool live = false;
+        for (int k = l; k - l < a.top && !live; k += kWave) {
+            float t;
+            live = __any(k < a.top && entry_of(a, index, teacher, k, &t) >= 0);
+        }
+        if (live) d += w;
+    }
+    d = l == 0 ? d : 0.0f;
+    d = block_all<OpSum>(d, lds, kLiveThreads / kWave);
+    if (threadIdx.x == 0) a.den[blockIdx.y * gridDim.x + blockIdx.x] = d;
+}
+
+// loss = sum of w row / sum of w, by one block.  With splits the rows' parts
+// are joined here first.
+__device__ void finish(const DistillArgs &a, float *lds)
+{
+    const int waves = blockDim.x / kWave;
     float d = 0.0f, l = 0.0f;
-    for (int64_t i = threadIdx.x; i < tokens; i += kDistillThreads) {
+    for (int64_t i = threadIdx.x; i < a.tokens; i += blockDim.x) {
         const float w = a.w[i];
+        if (!(w > 0.0f)) continue;
+        float loss = a.loss_of[i];
+        if (a.splits) {
+            const float *part = a.part + i * a.splits * 2;
+            float m = -FLT_MAX, s = 0.0f;
+            for (int k = 0; k < a.splits; ++k) m = fmaxf(m, part[2 * k]);
+            for (int k = 0; k < a.splits; ++k) s += part[2 * k + 1] * exp_of(a, part[2 * k] - m);
+            loss = a.tau * a.tau * (loss + ((m - a.ref[i]) * a.inv_tau + logf(s)));
+            int r = 0;
+            while (i >= a.first[r] + a.rows[r]) ++r;
+            if (a.row_loss.p[r]) st_elem<float>(a.row_loss.p[r], i - a.first[r], loss);
+        }
         d += w;
-        if (with_loss && w > 0.0f) l += w * a.loss_of[i];
+        l += w * loss;
     }
-    d = block_all<OpSum>(d, lds, kDistillThreads / kWave);
-    l = block_all<OpSum>(l, lds, kDistillThreads / kWave);
+    d = block_all<OpSum>(d, lds, waves);
+    l = block_all<OpSum>(l, lds, waves);
+    if (threadIdx.x == 0) *a.loss = d > 0.0f ? l / d : 0.0f;
+}
+
+__global__ void __launch_bounds__(kFarThreads) distill_total(DistillArgs a)
+{
+    __shared__ float lds[kMostWaves];
+    finish(a, lds);
+}
+
+// ---------------------------------------------------------------- a block to a token
+
+// What the waves of a block tell one another: their pairs, and what the first
+// knows of the teacher.
+struct Exchange {
+    float ms[kMostWaves], ss[kMostWaves];
+    float ref, base, den;
+    int alive;
+};
+
+// The block's first wave, past its share of the logits: the teacher.
+template <int DT, bool GRAD>
+__device__ __forceinline__ void teacher_wave(const DistillArgs &a, int r, int64_t row, const char *z, const Entries &en,
+                                             const FirstEntry &first, Exchange &x)
+{
+    const bool live = teacher_of<DT>(a, r, row, en, first, z, 0, a.vocab);
+    float ref;
+    const float base = divergence_of(a, en, &ref);
+    const float d = GRAD ? total_weight(a) : 0.0f;
     if (threadIdx.x == 0) {
-        if (with_loss) *a.loss = d > 0.0f ? l / d : 0.0f;
-        *a.den = d;
+        x.alive = live;
+        x.ref = ref;
+        x.base = base;
+        x.den = d;
     }
+}
+__device__ __forceinline__ void data_wave(Exchange &x, float m, float s)
+{
+    if (threadIdx.x % kWave == 0) {
+        x.ms[threadIdx.x / kWave] = m;
+        x.ss[threadIdx.x / kWave] = s;
+    }
+}
+// 2^(z k - c) with k = log2(e) / tau, one fused multiply-add to a logit.  c
+// stands for the largest logit m: c = fl(k m) with m within [-far, far], where
+// k far is finite.  The same c is taken out of every sum again, so its rounding
+// is no error: z k - c is rounded once.
+__device__ __forceinline__ float centre_of(const DistillArgs &a, float m)
+{
+    return __builtin_amdgcn_fmed3f(m, -a.far, a.far) * a.exp_scale;
+}
+__device__ __forceinline__ float exp_at(const DistillArgs &a, float z, float c)
+{
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(z, a.exp_scale, -c));
+}
+// Whether a sum of exp_at is one: not where logits lie beyond `far` (a row of
+// nothing but the type's lowest value, say) or are not finite.  Such rows go
+// through exp((z - m) / tau) with the subtraction first.
+__device__ __forceinline__ bool sane(float s) { return s >= FLT_MIN && s <= FLT_MAX; }
+
+// The pair of this thread's share of the n logits at z, the block's threads
+// taking U vectors each to a step: (m, s), or with FAST (c, s) of exp_at.
+template <int DT, bool FAST>
+__device__ __forceinline__ void stats_of(const DistillArgs &a, const char *z, int64_t n, float *first, float *s)
+{
+    constexpr int V = kVec<DT>, U = 4;
+    const int64_t step = (int64_t)blockDim.x * 16, vecs = n / V;
+    const uint32_t off = threadIdx.x * 16;
+    float own = -FLT_MAX, mark = FAST ? centre_of(a, -FLT_MAX) : own, sum = 0.0f;
+    auto add = [&](const u32x4 *v, int cnt) {
+#pragma unroll
+        for (int i = 0; i < cnt; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) own = fmaxf(own, value<V, DT>(v[i], e));
+        const float to = FAST ? centre_of(a, own) : own;
+        sum *= FAST ? __builtin_amdgcn_exp2f(mark - to) : exp_of(a, mark - to);
+        mark = to;
+#pragma unroll
+        for (int i = 0; i < cnt; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float x = value<V, DT>(v[i], e);
+                sum += FAST ? exp_at(a, x, to) : exp_of(a, x - to);
+            }
+    };
+    const char *p = z;
+    int64_t left = vecs;
+    for (; left >= U * (int64_t)blockDim.x; left -= U * (int64_t)blockDim.x, p += U * step) {
+        u32x4 v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[i] = ld_vec<false, u32x4>(p + i * step + off);
+        add(v, U);
+    }
+    if (left > 0) {   // vectors past the end: one before it, with exp = 0 in its place
+        u32x4 v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t k = i * (int64_t)blockDim.x + threadIdx.x;
+            v[i] = ld_vec<false, u32x4>(p + min64(k, left - 1) * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (i * (int64_t)blockDim.x + threadIdx.x >= left) {
+                const uint32_t none = DT == kF32 ? 0xff800000u : 0xff80ff80u;
+                v[i] = u32x4{none, none, none, none};
+            }
+        add(v, U);
+    }
+    const int64_t j = vecs * V + threadIdx.x;   // fewer than V are left
+    if (j < n) {
+        const float x = load_elem<DT>(z, j);
+        own = fmaxf(own, x);
+        const float to = FAST ? centre_of(a, own) : own;
+        sum = FAST ? sum * __builtin_amdgcn_exp2f(mark - to) + exp_at(a, x, to)
+                   : sum * exp_of(a, mark - to) + exp_of(a, x - to);
+        mark = to;
+    }
+    *first = mark;
+    *s = sum;
+}
+
+// dz of the n logits at z, entries aside: f exp_z(z).  The logits may lie where
+// dz does, so the last few are taken by element.
+template <int DT, class Exp>
+__device__ __forceinline__ void emit_of(const char *z, char *dz, int64_t n, float f, Exp &&exp_z)
+{
+    constexpr int V = kVec<DT>, U = 2;
+    const int64_t step = (int64_t)blockDim.x * 16, vecs = n / V;
+    const uint32_t off = threadIdx.x * 16;
+    auto put = [&](const u32x4 &v, char *to) {
+        float y[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] = exp_z(value<V, DT>(v, e)) * f;
+        st_values<V, DT, true>(to, y);
+    };
+    int64_t left = vecs, at = 0;
+    for (; left >= U * (int64_t)blockDim.x; left -= U * (int64_t)blockDim.x, at += U * step) {
+        u32x4 v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[i] = ld_vec<false, u32x4>(z + at + i * step + off);
+#pragma unroll
+        for (int i = 0; i < U; ++i) put(v[i], dz + at + i * step + off);
+    }
+    for (int64_t k = threadIdx.x; k < left; k += blockDim.x)
+        put(ld_vec<false, u32x4>(z + at + k * 16), dz + at + k * 16);
+    const int64_t j = vecs * V + threadIdx.x;
+    if (j < n) store_elem<DT>(dz, j, exp_z(load_elem<DT>(z, j)) * f);
+}
+
+// The token's loss and, with GRAD, its gradient by a block of `waves` waves, the
+// row read from memory: once for the loss, once more for the gradient.  The
+// teacher is looked up by the first wave unless `known`.
+template <int DT, bool GRAD, bool FAST>
+__device__ __forceinline__ bool row_far(const DistillArgs &a, int r, int64_t row, float w, const char *z, char *dz,
+                                        const Entries &en, Exchange &x, bool known)
+{
+    const int waves = blockDim.x / kWave;
+    FirstEntry first;
+    const bool look = threadIdx.x < kWave && !known;
+    if (look) first.load(a, r, row);
+    float m, s;
+    stats_of<DT, FAST>(a, z, a.vocab, &m, &s);
+    if (look) {
+        first.gather<DT>(a, z, 0, a.vocab);
+        teacher_wave<DT, GRAD>(a, r, row, z, en, first, x);
+    }
+    wave_join<FAST>(a, &m, &s);
+    data_wave(x, m, s);
+    __syncthreads();
+    if (FAST)
+        join_centres(x.ms, x.ss, waves, &m, &s);
+    else
+        join_pairs(a, x.ms, x.ss, waves, &m, &s);
+    if (FAST && !sane(s)) return false;
+    const bool live = x.alive != 0;
+    if (threadIdx.x == 0) {
+        // the row's largest logit over tau above r / tau, the product with r exact inside the fma
+        const float up = FAST ? kLn2 * __builtin_fmaf(-x.ref, a.exp_scale, m) : (m - x.ref) * a.inv_tau;
+        note_row(a, r, row, live ? w : 0.0f, live ? a.tau * a.tau * (x.base + (up + logf(s))) : 0.0f);
+    }
+    if (!GRAD) return true;
+    if (!live) {
+        emit_zeros<DT>(dz, 0, a.vocab);
+        return true;
+    }
+    const float c = a.scale * (w / x.den), inv_s = 1.0f / s;
+    auto exp_z = [&](float q) { return FAST ? exp_at(a, q, m) : exp_of(a, q - m); };
+    emit_of<DT>(z, dz, a.vocab, inv_s * c, exp_z);
+    __syncthreads();   // the entries' places are stored again
+    emit_entries<DT>(a, en, dz, exp_z, inv_s, c, 0, a.vocab);
+    return true;
 }
 
 template <int DT, bool GRAD>
-__global__ void __launch_bounds__(kDistillThreads) distill_rows(DistillArgs a)
+__global__ void __launch_bounds__(kFarThreads) distill_far(DistillArgs a, int64_t first_row)
 {
-    __shared__ float lds[kDistillThreads / kWave];
-    __shared__ float prob[DDP_MAX_TOP], zsel[DDP_MAX_TOP];
-    __shared__ int64_t at[DDP_MAX_TOP];
-    constexpr int waves = kDistillThreads / kWave;
-    const int r = blockIdx.y, tid = threadIdx.x;
-    const int64_t V = a.vocab;
-    const float inv_tau = 1.0f / a.tau;
-    for (int64_t row = blockIdx.x; row < a.rows[r]; row += gridDim.x) {
-        const char *z = a.z.p[r] + row * a.z.pitch;
-        char *dz = GRAD ? a.dz.p[r] + row * a.dz.pitch : nullptr;
-        const int64_t token = a.first[r] + row;
-        const float w = a.w[token];
-        if (!(w > 0.0f)) {
-            if (tid == 0) {
-                a.loss_of[token] = 0.0f;
-                if (a.row_loss.p[r]) st_elem<float>(a.row_loss.p[r], row, 0.0f);
+    const Entries en = entries_of(a);
+    __shared__ Exchange x;
+    const int r = blockIdx.y;
+    if (first_row + blockIdx.x >= a.rows[r]) return;
+    const int64_t row = row_of_block(first_row + blockIdx.x, a.rows[r]);
+    const float w = weight_of(a, r, row);
+    char *dz = GRAD ? a.dz.p[r] + row * a.dz.pitch : nullptr;
+    if (w == 0.0f) {
+        if (threadIdx.x == 0) note_row(a, r, row, 0.0f, 0.0f);
+        if (GRAD) emit_zeros<DT>(dz, 0, a.vocab);
+        return;
+    }
+    const char *z = a.z.p[r] + row * a.z.pitch;
+    if (row_far<DT, GRAD, true>(a, r, row, w, z, dz, en, x, false)) return;
+    __syncthreads();
+    row_far<DT, GRAD, false>(a, r, row, w, z, dz, en, x, true);
+}
+
+// What follows takes the vectors' elements apart anew: kept apart from one use
+// to the next they would hold twice the registers.
+template <int NV>
+__device__ __forceinline__ void again(u32x4 (&v)[NV])
+{
+#pragma unroll
+    for (int i = 0; i < NV; ++i) asm volatile("" : "+v"(v[i]));
+}
+
+// The gradient with the row in registers, NV 16-byte vectors to a thread: f32
+// holds the exponentials, bf16 the packed logits (half the registers, so twice
+// the rows on a CU) and takes each exponential twice.
+template <int DT, int NV, bool NT>
+__global__ void __launch_bounds__(kMostWaves * kWave) __attribute__((amdgpu_waves_per_eu(4)))
+distill_held(DistillArgs a, int64_t first_row)
+{
+    constexpr int V = kVec<DT>, size = kSize<DT>;
+    constexpr int U = DT == kF32 ? NV : 2;   // vectors to a step of the running pair
+    const Entries en = entries_of(a);
+    __shared__ Exchange x;
+    const int r = blockIdx.y, threads = blockDim.x, waves = threads / kWave;
+    if (first_row + blockIdx.x >= a.rows[r]) return;
+    const int64_t row = row_of_block(first_row + blockIdx.x, a.rows[r]);
+    const float w = weight_of(a, r, row);
+    char *dz = a.dz.p[r] + row * a.dz.pitch;
+    if (w == 0.0f) {
+        if (threadIdx.x == 0) note_row(a, r, row, 0.0f, 0.0f);
+        emit_zeros<DT>(dz, 0, a.vocab);
+        return;
+    }
+    const char *z = a.z.p[r] + row * a.z.pitch;
+    const int n = (int)a.vocab;
+    FirstEntry first;
+    if (threadIdx.x < kWave) first.load(a, r, row);
+    u32x4 v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        v[i] = ld_vec<NT, u32x4>(z + piece_of<V>(i * threads + (int)threadIdx.x, n).at * size);
+    if (threadIdx.x < kWave) first.gather<DT>(a, z, 0, n);
+    const int wave_end = __builtin_amdgcn_readfirstlane(((int)threadIdx.x | (kWave - 1)) + 1);
+    float own = -FLT_MAX, s = 0.0f, c_own = 0.0f;
+#pragma unroll
+    for (int g = 0; g < NV; g += U) {
+#pragma unroll
+        for (int i = g; i < g + U; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) own = fmaxf(own, value<V, DT>(v[i], e));
+        const float c = centre_of(a, own);
+        if (g) s *= __builtin_amdgcn_exp2f(c_own - c);
+        c_own = c;
+#pragma unroll
+        for (int i = g; i < g + U; ++i) {
+            float ex[V], t = 0.0f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                ex[e] = exp_at(a, value<V, DT>(v[i], e), c);
+                t += ex[e];
             }
-            if (GRAD)
-                for (int64_t j = tid; j < V; j += kDistillThreads) store_elem<DT>(dz, j, 0.0f);
-            continue;
+            if ((i * threads + wave_end) * V > n) {   // this wave's vectors reach the row's end
+                int t0 = threadIdx.x;
+                asm volatile("" : "+v"(t0));
+                const int skip = (int)piece_of<V>(i * threads + t0, n).skip;
+                t = 0.0f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) t += e >= skip ? ex[e] : 0.0f;
+            }
+            s += t;
+            if (DT == kF32) {   // in place of the logits
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][e] = __float_as_uint(ex[e]);
+            }
         }
-        float m = -INFINITY;
-        for (int64_t j = tid; j < V; j += kDistillThreads) m = fmaxf(m, load_elem<DT>(z, j));
-        m = block_all<OpMax>(m, lds, waves);
-        float sum = 0.0f;
-        for (int64_t j = tid; j < V; j += kDistillThreads)
-            sum += expf((load_elem<DT>(z, j) - m) * inv_tau);
-        sum = block_all<OpSum>(sum, lds, waves);
-        // the teacher
-        float tm = -INFINITY;
+    }
+    if (threadIdx.x < kWave) teacher_wave<DT, true>(a, r, row, z, en, first, x);
+    float c_row = c_own, s_row = s;
+    wave_join<true>(a, &c_row, &s_row);
+    data_wave(x, c_row, s_row);
+    __syncthreads();
+    join_centres(x.ms, x.ss, waves, &c_row, &s_row);
+    if (!sane(s_row)) {   // once more, from the row as it still lies in memory
         __syncthreads();
-        for (int k = tid; k < a.top; k += kDistillThreads) {
-            float t = 0.0f;
-            const int64_t j = entry_of(a, r, row, k, &t);
-            at[k] = j;
-            prob[k] = t;
-            if (j >= 0) {
-                tm = fmaxf(tm, t);
-                zsel[k] = load_elem<DT>(z, j);
-            }
+        row_far<DT, true, false>(a, r, row, w, z, dz, en, x, true);
+        return;
+    }
+    const bool live = x.alive != 0;
+    if (threadIdx.x == 0) {
+        const float up = kLn2 * __builtin_fmaf(-x.ref, a.exp_scale, c_row);
+        note_row(a, r, row, live ? w : 0.0f, live ? a.tau * a.tau * (x.base + (up + logf(s_row))) : 0.0f);
+    }
+    if (!live) {
+        emit_zeros<DT>(dz, 0, a.vocab);
+        return;
+    }
+    const float c = a.scale * (w / x.den), inv_s = 1.0f / s_row;
+    const float f = DT == kF32 ? __builtin_amdgcn_exp2f(c_own - c_row) * inv_s * c : inv_s * c;
+    int t0 = threadIdx.x;
+    asm volatile("" : "+v"(t0));   // the vectors' places are found anew, not kept in registers
+    if (DT == kBF16) again(v);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float y[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            y[e] = (DT == kF32 ? value<V, DT>(v[i], e) : exp_at(a, value<V, DT>(v[i], e), c_row)) * f;
+        const Piece pc = piece_of<V>(i * threads + t0, n);
+        if (owned<V>(pc)) st_values<V, DT, NT>(dz + pc.at * size, y);
+    }
+    __syncthreads();   // the entries' places are stored again
+    emit_entries<DT>(a, en, dz, [&](float q) { return exp_at(a, q, c_row); }, inv_s, c, 0, n);
+}
+
+// ---------------------------------------------------------------- several blocks to a token
+
+// First pass: (m, s) of a split; split 0 also looks up the teacher and notes the
+// row's weight and its loss but for m and s.
+template <int DT>
+__global__ void __launch_bounds__(kPartThreads) distill_part(DistillArgs a)
+{
+    const Entries en = entries_of(a);
+    __shared__ float ms[kMostWaves], ss[kMostWaves];
+    const int r = blockIdx.z, split = blockIdx.x;
+    const int64_t row = blockIdx.y;
+    if (row >= a.rows[r]) return;
+    const int64_t token = a.first[r] + row;
+    const float w = weight_of(a, r, row);
+    if (w == 0.0f) {
+        if (split == 0 && threadIdx.x == 0) note_row(a, r, row, 0.0f, 0.0f);
+        return;
+    }
+    const char *z = a.z.p[r] + row * a.z.pitch;
+    const int64_t lo = split * a.seg, hi = split + 1 == a.splits ? a.vocab : lo + a.seg;
+    float m, s;
+    FirstEntry first;
+    const bool look = split == 0 && threadIdx.x < kWave;
+    if (look) first.load(a, r, row);
+    stats_of<DT, false>(a, z + lo * kSize<DT>, hi - lo, &m, &s);
+    wave_join<false>(a, &m, &s);
+    if (threadIdx.x % kWave == 0) {
+        ms[threadIdx.x / kWave] = m;
+        ss[threadIdx.x / kWave] = s;
+    }
+    if (look) {
+        first.gather<DT>(a, z, 0, a.vocab);
+        const bool live = teacher_of<DT>(a, r, row, en, first, z, 0, a.vocab);
+        float ref = 0.0f, base = 0.0f;
+        if (live) base = divergence_of(a, en, &ref);
+        if (threadIdx.x == 0) {
+            note_row(a, r, row, live ? w : 0.0f, live ? base : 0.0f);
+            a.ref[token] = ref;
         }
-        tm = block_all<OpMax>(tm, lds, waves);
-        float mass = 0.0f;
-        for (int k = tid; k < a.top; k += kDistillThreads)
-            if (at[k] >= 0) mass += expf((prob[k] - tm) * inv_tau);
-        mass = block_all<OpSum>(mass, lds, waves);
-        const float lmass = logf(mass), lsum = logf(sum);
-        float kl = 0.0f;
-        for (int k = tid; k < a.top; k += kDistillThreads) {
-            if (at[k] < 0) continue;
-            const float lp = (prob[k] - tm) * inv_tau - lmass;
-            const float p = expf((prob[k] - tm) * inv_tau) / mass;
-            if (p > 0.0f) kl += p * (lp - ((zsel[k] - m) * inv_tau - lsum));
-            prob[k] = p;
-        }
-        kl = block_all<OpSum>(kl, lds, waves);
-        const float loss = a.tau * a.tau * kl;
-        if (tid == 0) {
-            a.loss_of[token] = loss;
-            if (a.row_loss.p[r]) st_elem<float>(a.row_loss.p[r], row, loss);
-        }
-        if (!GRAD) continue;
-        const float c = a.scale * (w / *a.den), inv_sum = 1.0f / sum;
-        for (int64_t j = tid; j < V; j += kDistillThreads)
-            store_elem<DT>(dz, j, c * (expf((load_elem<DT>(z, j) - m) * inv_tau) * inv_sum));
-        __syncthreads();   // the entries' places are written again below
-        for (int k = tid; k < a.top; k += kDistillThreads) {
-            if (at[k] < 0) continue;
-            float p = 0.0f;
-            for (int i = 0; i < a.top; ++i)
-                if (at[i] == at[k]) p += prob[i];
-            store_elem<DT>(dz, at[k], c * (expf((zsel[k] - m) * inv_tau) * inv_sum - p));
-        }
-        __syncthreads();   // prob, zsel and at are used again
+    }
+    __syncthreads();
+    join_pairs(a, ms, ss, kPartThreads / kWave, &m, &s);
+    if (threadIdx.x == 0) {
+        a.part[(token * a.splits + split) * 2] = m;
+        a.part[(token * a.splits + split) * 2 + 1] = s;
     }
 }
 
-int64_t distill_bytes(int64_t total) { return 16 + (2 * total * 4 + 15) / 16 * 16; }
+// Second pass: the gradient of a split.  One block more, past the last rank's
+// first row, sums up the loss.
+template <int DT>
+__global__ void __launch_bounds__(kPartThreads) distill_emit(DistillArgs a)
+{
+    const Entries en = entries_of(a);
+    __shared__ float lds[kMostWaves];
+    const int r = blockIdx.z, split = blockIdx.x;
+    if (split == a.splits) {
+        if (r == 0 && blockIdx.y == 0) finish(a, lds);
+        return;
+    }
+    const int64_t row = blockIdx.y;
+    if (row >= a.rows[r]) return;
+    const int64_t token = a.first[r] + row;
+    const int64_t lo = split * a.seg, hi = split + 1 == a.splits ? a.vocab : lo + a.seg;
+    char *dz = a.dz.p[r] + row * a.dz.pitch;
+    const float w = a.w[token];
+    if (w == 0.0f) {
+        emit_zeros<DT>(dz, lo, hi);
+        return;
+    }
+    const char *z = a.z.p[r] + row * a.z.pitch;
+    FirstEntry first;
+    if (threadIdx.x < kWave) first.load(a, r, row);
+    // every wave joins the row's parts for itself
+    const int l = threadIdx.x % kWave;
+    float m = -FLT_MAX, s = 0.0f;
+    if (l < a.splits) {
+        m = a.part[(token * a.splits + l) * 2];
+        s = a.part[(token * a.splits + l) * 2 + 1];
+    }
+    wave_join<false>(a, &m, &s);
+    float d = 0.0f;
+    for (int64_t i = threadIdx.x; i < a.tokens; i += kPartThreads) d += a.w[i];
+    d = block_all<OpSum>(d, lds, kPartThreads / kWave);
+    if (threadIdx.x < kWave) {
+        first.gather<DT>(a, z, lo, hi);
+        teacher_of<DT>(a, r, row, en, first, z, lo, hi);
+    }
+    __syncthreads();   // the logits at the entries are read before any is written
+    const float c = a.scale * (w / d), inv_s = 1.0f / s;
+    auto exp_z = [&](float q) { return exp_of(a, q - m); };
+    emit_of<DT>(z + lo * kSize<DT>, dz + lo * kSize<DT>, hi - lo, inv_s * c, exp_z);
+    __syncthreads();
+    emit_entries<DT>(a, en, dz, exp_z, inv_s, c, lo, hi);
+}
 
-constexpr int64_t kMostGridRows = 1 << 16;
+// ---------------------------------------------------------------- host
+
+// Blocks to a token: enough to give the 256 CUs two blocks each, of at least
+// 2048 logits; 0 where one block to a token does.
+struct Splits {
+    int32_t n;
+    int64_t seg;
+};
+Splits splits_of(int64_t tokens, int64_t vocab)
+{
+    if (tokens == 0 || tokens >= 256 || vocab < 4096) return {0, 0};
+    int64_t n = std::min<int64_t>({kMostSplits, (512 + tokens - 1) / tokens, vocab / 2048});
+    const int64_t seg = ((vocab + n - 1) / n + 7) / 8 * 8;
+    n = (vocab + seg - 1) / seg;
+    return {(int32_t)n, seg};
+}
+
+int64_t distill_bytes(int64_t tokens, int64_t vocab)
+{
+    const int64_t floats = kMostLiveBlocks + 3 * tokens + 2 * tokens * splits_of(tokens, vocab).n;
+    return (floats * 4 + 15) / 16 * 16;
+}
+
+constexpr int64_t kMostThreads = kMostWaves * kWave;
+
+// Threads of a block that steps through a row of `vecs` vectors, at most `most`.
+int far_threads(int64_t vecs, int most)
+{
+    return (int)std::min<int64_t>(most, (vecs + kWave - 1) / kWave * kWave);
+}
+
+template <int DT, bool NT>
+ddp_status_t launch_grad(const DistillArgs &a, int64_t most, hipStream_t st)
+{
+    constexpr int V = kVec<DT>;
+    const int64_t vecs = (a.vocab + V - 1) / V;
+    constexpr int kBig = DT == kF32 ? 16 : 8;   // 64 exponentials to a thread
+    const int nv = a.vocab < V || vecs > kBig * kMostThreads ? 0 : vecs <= 2 * 256 ? 2 : vecs <= kBig / 2 * 256 ? kBig / 2 : kBig;
+    const int threads = nv ? (int)((vecs + nv * kWave - 1) / (nv * kWave)) * kWave : far_threads(vecs, kFarThreads);
+    const unsigned lds = entry_bytes(a.top);
+    return launch_split(most, threads, "distillation kernel launch", [&](int64_t b0, unsigned nb) {
+        const dim3 g(nb, (unsigned)a.n_ranks);
+        if (nv == 2)
+            distill_held<DT, 2, NT><<<g, threads, lds, st>>>(a, b0);
+        else if (nv == kBig / 2)
+            distill_held<DT, kBig / 2, NT><<<g, threads, lds, st>>>(a, b0);
+        else if (nv == kBig)
+            distill_held<DT, kBig, NT><<<g, threads, lds, st>>>(a, b0);
+        else
+            distill_far<DT, true><<<g, threads, lds, st>>>(a, b0);
+    });
+}
+
+template <int DT>
+ddp_status_t launch_rows(const DistillArgs &a, int64_t most, bool grad, bool nt, hipStream_t st)
+{
+    if (grad) return nt ? launch_grad<DT, true>(a, most, st) : launch_grad<DT, false>(a, most, st);
+    const int threads = far_threads((a.vocab + kVec<DT> - 1) / kVec<DT>, 256);
+    return launch_split(most, threads, "distillation kernel launch", [&](int64_t b0, unsigned nb) {
+        distill_far<DT, false><<<dim3(nb, (unsigned)a.n_ranks), threads, entry_bytes(a.top), st>>>(a, b0);
+    });
+}
 
 ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_t vocab,
                          const ddp_rows_t *logits, int dtype, int32_t top, const ddp_rows_t *teacher,
@@ -183,11 +860,12 @@ ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_
         (index_bytes != 4 && index_bytes != 8) || !(temperature > 0.0f) ||
         !std::isfinite(temperature) || !loss)
         return DDP_ERR_INVALID_ARG;
-    if (top > DDP_MAX_TOP) return DDP_ERR_UNSUPPORTED;
+    if (top > DDP_MAX_TOP || vocab > INT32_MAX || temperature < 1e-6f || temperature > 1e6f)
+        return DDP_ERR_UNSUPPORTED;
     if (total > 0 && (!logits || !logits->rank || !teacher || !teacher->rank || !index ||
                       !index->rank || (grad && (!dlogits || !dlogits->rank))))
         return DDP_ERR_INVALID_ARG;
-    const int64_t need = distill_bytes(total);
+    const int64_t need = distill_bytes(total, vocab);
     if (!workspace || !aligned(workspace, 16)) return DDP_ERR_INVALID_ARG;
     if (workspace_bytes < need) return DDP_ERR_CAPACITY;
     const int esz = dtype_size(dtype), tsz = dtype_size(teacher_dtype);
@@ -219,37 +897,56 @@ ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_
     }
     std::memcpy(a.rows, rows, sizeof(int64_t) * (size_t)n_ranks);
     for (int r = 1; r < n_ranks; ++r) a.first[r] = a.first[r - 1] + rows[r - 1];
+    const Splits sp = splits_of(total, vocab);
+    a.tokens = total;
     a.vocab = vocab;
+    a.seg = sp.seg;
     a.n_ranks = n_ranks;
     a.top = top;
+    a.splits = sp.n;
     a.tdt = teacher_dtype;
     a.index_bytes = index_bytes;
     a.tau = temperature;
     a.scale = grad_scale * (float)n_ranks * temperature;
+    a.inv_tau = 1.0f / temperature;
+    a.exp_scale = (float)(1.4426950408889634 / (double)temperature);   // log2(e) / tau
+    a.far = std::min(0x1p100f, 0x1p120f / a.exp_scale);
     a.den = static_cast<float *>(workspace);
-    a.w = a.den + 4;
+    a.w = a.den + kMostLiveBlocks;
     a.loss_of = a.w + total;
+    a.ref = a.loss_of + total;
+    a.part = a.ref + total;
     a.loss = loss;
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    if (total > 0) {
-        const int64_t wb = std::min<int64_t>((most + kDistillThreads - 1) / kDistillThreads, 256);
-        distill_weights<<<dim3((unsigned)wb, (unsigned)n_ranks), kDistillThreads, 0, hs>>>(a);
-        if ((st = launched("distillation weight kernel launch")) != DDP_OK) return st;
-        if (grad) {
-            distill_total<<<1, kDistillThreads, 0, hs>>>(a, total, 0);
-            if ((st = launched("distillation total kernel launch")) != DDP_OK) return st;
-        }
-        const dim3 g((unsigned)std::min(most, kMostGridRows), (unsigned)n_ranks);
-        if (dtype == DDP_F32) {
-            if (grad) distill_rows<kF32, true><<<g, kDistillThreads, 0, hs>>>(a);
-            else distill_rows<kF32, false><<<g, kDistillThreads, 0, hs>>>(a);
-        } else {
-            if (grad) distill_rows<kBF16, true><<<g, kDistillThreads, 0, hs>>>(a);
-            else distill_rows<kBF16, false><<<g, kDistillThreads, 0, hs>>>(a);
-        }
+    if (sp.n) {
+        const dim3 g((unsigned)sp.n, (unsigned)most, (unsigned)n_ranks);
+        if (dtype == DDP_F32)
+            distill_part<kF32><<<g, kPartThreads, entry_bytes(top), hs>>>(a);
+        else
+            distill_part<kBF16><<<g, kPartThreads, entry_bytes(top), hs>>>(a);
         if ((st = launched("distillation kernel launch")) != DDP_OK) return st;
+        if (grad) {
+            const dim3 e((unsigned)sp.n + 1, (unsigned)most, (unsigned)n_ranks);
+            if (dtype == DDP_F32)
+                distill_emit<kF32><<<e, kPartThreads, entry_bytes(top), hs>>>(a);
+            else
+                distill_emit<kBF16><<<e, kPartThreads, entry_bytes(top), hs>>>(a);
+            return launched("distillation gradient kernel launch");
+        }
+    } else if (total > 0) {
+        if (grad) {
+            const int64_t per = kLiveThreads / kWave;
+            const int64_t lb = std::max<int64_t>(1, std::min<int64_t>((most + per - 1) / per,
+                                                                      kMostLiveBlocks / n_ranks));
+            a.live_blocks = (int32_t)(lb * n_ranks);
+            distill_live<<<dim3((unsigned)lb, (unsigned)n_ranks), kLiveThreads, 0, hs>>>(a);
+            if ((st = launched("distillation weight kernel launch")) != DDP_OK) return st;
+        }
+        const bool nt = total * vocab * esz * (grad ? 2 : 1) >= (int64_t)256 << 20;
+        st = dtype == DDP_F32 ? launch_rows<kF32>(a, most, grad, nt, hs) : launch_rows<kBF16>(a, most, grad, nt, hs);
+        if (st != DDP_OK) return st;
     }
-    distill_total<<<1, kDistillThreads, 0, hs>>>(a, total, 1);
+    distill_total<<<1, kFarThreads, 0, hs>>>(a);
     return launched("distillation total kernel launch");
 }
 
@@ -261,7 +958,7 @@ int64_t ddp_distill_workspace(const int64_t *rows, int32_t n_ranks, int64_t voca
 {
     int64_t total, most;
     if (check_shape(rows, n_ranks, vocab, &total, &most) != DDP_OK) return -1;
-    return distill_bytes(total);
+    return distill_bytes(total, vocab);
 }
 
 ddp_status_t ddp_distill_loss(const int64_t *rows, int32_t n_ranks, int64_t vocab,

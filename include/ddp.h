@@ -518,7 +518,7 @@ DDP_API int64_t ddp_rms_norm_grad_workspace(const int64_t *rows, int32_t n_ranks
 
 /* Distillation: the divergence of a student's distribution over `vocab` from
  * a teacher known by its `top` largest logits of each token.
- *   an entry is live      when 0 <= index < vocab and its logit > -infinity;
+ *   an entry is live      when 0 <= index < vocab and its logit > -infinity (so is no NaN);
  *                         what any other entry holds is not looked at
  *   a token is live       when it has a live entry and its weight is > 0
  *   p = softmax(teacher / temperature) over the token's live entries
@@ -538,14 +538,14 @@ DDP_API int64_t ddp_rms_norm_grad_workspace(const int64_t *rows, int32_t n_ranks
  *   token_weight  host array [n_ranks] of device pointers to rows[r] floats,
  *                 or NULL for ones.  A weight that is not > 0 (NaN included)
  *                 masks its token
- *   temperature   > 0
+ *   temperature   1e-6 to 1e6
  *   loss          device, one float
  *   row_loss      host array [n_ranks] of device pointers to rows[r] floats, or
  *                 NULL
  *   workspace     ddp_distill_workspace(rows, n_ranks, vocab) bytes
  * Sums are taken in f32 in an order that depends on the shape alone.
- * Errors: INVALID_ARG, UNSUPPORTED (top or rank count beyond the library's),
- * OVERFLOW, ALIAS, CAPACITY, HIP. */
+ * Errors: INVALID_ARG, UNSUPPORTED (a top, rank count, temperature or vocabulary
+ * (2^31 - 1) beyond the library's), OVERFLOW, ALIAS, CAPACITY, HIP. */
 DDP_API ddp_status_t ddp_distill_loss(const int64_t *rows, int32_t n_ranks, int64_t vocab,
                                       const ddp_rows_t *logits, ddp_dtype_t dtype, int32_t top,
                                       const ddp_rows_t *teacher, ddp_dtype_t teacher_dtype,

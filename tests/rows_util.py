@@ -142,7 +142,7 @@ def distill_64(logits, teacher, index, weight, tau, grad_scale=1.0):
         vocab = z.shape[1]
         idx = index[r].long()
         t = teacher[r].double()
-        ok = (idx >= 0) & (idx < vocab) & ~(t == -math.inf)
+        ok = (idx >= 0) & (idx < vocab) & (t > -math.inf)
         w = torch.ones(z.shape[0], dtype=torch.float64, device=z.device) if weight is None \
             else weight[r].double()
         live = ok.any(1) & (w > 0)

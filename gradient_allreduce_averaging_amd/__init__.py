@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import List, Optional, Sequence
 
 import torch
@@ -134,7 +135,8 @@ def _load():
                               ctypes.c_int32, vp, ctypes.c_int, vp, ctypes.c_int32, vp,
                               ctypes.c_float, ctypes.c_float, vp, vp, vp, vp, ctypes.c_int64, vp],
                              ctypes.c_int),
-        "ddp_distill_workspace": ([c_i64p, ctypes.c_int32, ctypes.c_int64], ctypes.c_int64),
+        "ddp_distill_workspace": ([c_i64p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32],
+                                  ctypes.c_int64),
         "ddp_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "ddp_abi_version": ([], ctypes.c_int32),
         "ddp_last_error": ([], ctypes.c_char_p),
@@ -607,27 +609,36 @@ class _Tokens:
     laid out as the C call takes them.  ``like[r]`` is rank r's matrix [..., width],
     its rows one fixed distance apart; the other operands have its shape.
 
-    All pointer arrays and ddp_rows_t structures of a call go into one buffer of
+    All pointer arrays and ddp_rows_t structures of a call go into one array of
     64-bit words: an operand is known by its place there (``ref``) until ``done`` makes the
-    buffer."""
+    array.  (A call on small tensors is bound by this work: 3 us of about 8.)"""
+
+    __slots__ = ("device", "n", "rows", "width", "words", "fix")
 
     def __init__(self, like: Sequence):
-        self.device = torch.cuda.current_device()
+        self.device = torch._C._cuda_getDevice()
         self.n = len(like)
         if self.n == 0:
             raise ValueError("no ranks")
-        self.rows = []
-        self.width = 0
+        rows = []
+        width = 0
         for t in like:
             shape = t.shape
-            if not shape:
+            if len(shape) == 2:
+                n, w = shape
+            elif shape:
+                w = shape[-1]
+                n = t.numel() // max(w, 1)
+            else:
                 raise ValueError("a rank's tensor needs a dimension for the width")
-            self.width = self.width or shape[-1]
-            if self.width < 1:
-                raise ValueError("the width is 0")
-            self.rows.append(shape[0] if len(shape) == 2 else t.numel() // self.width)
-        self.words = list(self.rows)
-        self.fix = []          # words that hold the address of another word
+            width = width or w
+            rows.append(n)
+        if width < 1:
+            raise ValueError("the width is 0")
+        self.rows = rows
+        self.width = width
+        self.words = rows.copy()
+        self.fix = []          # (word, the word whose address it holds)
 
     def _on_device(self, t):
         if t.get_device() != self.device:
@@ -639,42 +650,46 @@ class _Tokens:
             return None, None
         if len(ts) != self.n:
             raise ValueError(f"{what}: one tensor per rank is required")
-        dtype, stride, device, words = ts[0].dtype, None, self.device, self.words
+        dtype, device, words = ts[0].dtype, self.device, self.words
         if dtype not in codes:
             raise TypeError(f"{what}: unsupported dtype {dtype}")
         first = len(words)
+        stride = None
         for t, n in zip(ts, self.rows):
             if t.get_device() != device:
                 self._on_device(t)
             if t.dtype != dtype:
                 raise ValueError(f"{what}: the ranks differ in dtype")
-            shape = t.shape
-            if len(shape) == 2:
-                fits = shape[0] == n and shape[1] == width
-                strides = t.stride()
+            if t.dim() == 2:
+                pitch, step = t.stride()
+                if t.shape != (n, width):
+                    raise ValueError(f"{what}: {n} rows of {width} elements are required, got {tuple(t.shape)}")
             else:
-                fits = len(shape) > 0 and shape[-1] == width and t.numel() == n * width
-                strides = None
-            if not fits:
-                raise ValueError(f"{what}: {n} rows of {width} elements are required, got {tuple(shape)}")
+                pitch, step = self._flat_stride(t, n, width, what)
             if n > 0:
-                if strides is None:
-                    try:
-                        strides = t.view(-1, width).stride()
-                    except RuntimeError:
-                        raise ValueError(f"{what}: the rows are not one fixed distance apart") from None
-                if width > 1 and strides[1] != 1:
+                if step != 1 and width > 1:
                     raise ValueError(f"{what}: the elements of a row are not consecutive")
-                if n > 1:
-                    if stride is None:
-                        stride = strides[0]
-                    elif stride != strides[0]:
+                if n > 1 and pitch != stride:
+                    if stride is not None:
                         raise ValueError(f"{what}: the ranks differ in row stride")
+                    stride = pitch
             words.append(t.data_ptr())
-        self.fix.append((len(words), first))
+        at = len(words)
+        self.fix.append((at, first))
         words.append(0)
         words.append(width if stride is None else stride)
-        return dtype, len(words) - 2
+        return dtype, at
+
+    @staticmethod
+    def _flat_stride(t, n, width, what):
+        """Strides of a tensor of other than two dimensions as a matrix."""
+        shape = t.shape
+        if not shape or shape[-1] != width or t.numel() != n * width:
+            raise ValueError(f"{what}: {n} rows of {width} elements are required, got {tuple(shape)}")
+        try:
+            return t.view(-1, width).stride()
+        except RuntimeError:
+            raise ValueError(f"{what}: the rows are not one fixed distance apart") from None
 
     def vectors(self, ts, what: str, length=None, codes=_ONE_F32):
         """(dtype, ref of the pointer array) of one vector per rank: ``length`` elements, or one
@@ -711,13 +726,11 @@ class _Tokens:
             raise ValueError(f"{what}: tensor is not contiguous")
         return codes[t.dtype], t.data_ptr()
 
-    def workspace(self, t, need, stream):
+    def workspace(self, t, need, stream, *more):
         """(address, bytes, tensor) of the caller's workspace, or of a new one of need(rows, n,
-        width) bytes that belongs to the call's stream."""
+        width, *more) bytes that belongs to the call's stream."""
         if t is None:
-            nbytes = need((ctypes.c_int64 * self.n)(*self.rows), self.n, self.width)
-            if nbytes < 0:
-                raise DDPError(1, need.__name__)
+            nbytes = _workspace_bytes(need, self.rows, self.width, *more)
             if stream is None:
                 t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
             else:
@@ -736,15 +749,13 @@ class _Tokens:
         return _stream_handle(stream)
 
     def done(self, *refs):
-        """The buffer (to be kept until the call returns) and the address of each ref, None for
+        """The array (to be kept until the call returns) and the address of each ref, None for
         None; ref 0 is the row counts."""
-        buf = (ctypes.c_int64 * len(self.words))()
-        base = ctypes.addressof(buf)
-        words = self.words
+        words = array("q", self.words)
+        base = words.buffer_info()[0]
         for at, first in self.fix:
             words[at] = base + 8 * first
-        buf[:] = words
-        return buf, [None if r is None else base + 8 * r for r in refs]
+        return words, [None if r is None else base + 8 * r for r in refs]
 
 
 def rms_norm(x: Sequence, weight, out: Sequence, residual: Optional[Sequence] = None,
@@ -763,16 +774,16 @@ def rms_norm(x: Sequence, weight, out: Sequence, residual: Optional[Sequence] = 
         raise ValueError("residual and sum_out must have x's dtype")
     _, sc = tk.vectors(scale, "scale")
     wdt, wp = tk.shared(weight, "weight", width, _FLOATS)
-    buf, (rows, xr, rr, sr, yr, sc) = tk.done(0, xr, rr, sr, yr, sc)
+    words, (rows, xr, rr, sr, yr, sc) = tk.done(0, xr, rr, sr, yr, sc)
     st = lib.ddp_rms_norm(rows, tk.n, width, xr, rr, _FLOATS[dt], wp, wdt, eps, sr, yr, _NORM_OUT[ydt], sc,
                           tk.stream(stream))
     if st:
         _check(st, "ddp_rms_norm")
 
 
-def _workspace_bytes(fn, rows: Sequence[int], width: int) -> int:
+def _workspace_bytes(fn, rows: Sequence[int], width: int, *more) -> int:
     n = len(rows)
-    need = fn((ctypes.c_int64 * n)(*rows), n, int(width))
+    need = fn((ctypes.c_int64 * n)(*rows), n, int(width), *more)
     if need < 0:
         raise DDPError(1, fn.__name__)
     return need
@@ -802,7 +813,7 @@ def rms_norm_grad(s: Sequence, weight, dy: Sequence, dx: Sequence, dsum: Optiona
     ws, nbytes, keep = None, 0, None
     if dweight is not None:
         ws, nbytes, keep = tk.workspace(workspace, lib.ddp_rms_norm_grad_workspace, stream)
-    buf, (rows, sr, yr, dr, xr, wg) = tk.done(0, sr, yr, dr, xr, wg)
+    words, (rows, sr, yr, dr, xr, wg) = tk.done(0, sr, yr, dr, xr, wg)
     st = lib.ddp_rms_norm_grad(rows, tk.n, width, sr, _FLOATS[dt], wp, wdt, eps, yr, _FLOATS[ydt], dr, xr, wg,
                                F32 if gdt is None else _FLOATS[gdt], 1 if accumulate else 0, ws, nbytes,
                                tk.stream(stream))
@@ -810,10 +821,10 @@ def rms_norm_grad(s: Sequence, weight, dy: Sequence, dx: Sequence, dsum: Optiona
         _check(st, "ddp_rms_norm_grad")
 
 
-def distill_workspace(rows: Sequence[int], vocab: int) -> int:
+def distill_workspace(rows: Sequence[int], vocab: int, top: int) -> int:
     """Bytes of workspace ``distill_loss`` and ``distill_grad`` need for ranks of
-    ``rows[r]`` tokens."""
-    return _workspace_bytes(lib.ddp_distill_workspace, rows, vocab)
+    ``rows[r]`` tokens with ``top`` teacher entries each."""
+    return _workspace_bytes(lib.ddp_distill_workspace, rows, vocab, int(top))
 
 
 def _distill(logits, teacher, index, dlogits, loss, row_loss, token_weight, temperature, grad_scale,
@@ -832,8 +843,8 @@ def _distill(logits, teacher, index, dlogits, loss, row_loss, token_weight, temp
     gdt, gr = tk.matrix(dlogits, "dlogits", _FLOATS, vocab)
     if (gdt or dt) != dt:
         raise ValueError("dlogits must have the logits' dtype")
-    ws, nbytes, keep = tk.workspace(workspace, lib.ddp_distill_workspace, stream)
-    buf, (rows, zr, tr, ir, tw, rl, gr) = tk.done(0, zr, tr, ir, tw, rl, gr)
+    ws, nbytes, keep = tk.workspace(workspace, lib.ddp_distill_workspace, stream, top)
+    words, (rows, zr, tr, ir, tw, rl, gr) = tk.done(0, zr, tr, ir, tw, rl, gr)
     if dlogits is None:
         st = lib.ddp_distill_loss(rows, tk.n, vocab, zr, _FLOATS[dt], top, tr, _FLOATS[tdt], ir,
                                   _INDICES[idt], tw, temperature, lp, rl, ws, nbytes, tk.stream(stream))

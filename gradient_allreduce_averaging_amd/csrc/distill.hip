@@ -37,31 +37,36 @@ using namespace ddp_detail;
 namespace {
 
 constexpr int kFarThreads = 1024;     // distill_far, and the last sum of the loss
+constexpr int kLossThreads = 512;     // distill_row
 constexpr int kPartThreads = 256;     // distill_part, distill_emit
-constexpr int kLiveThreads = 256;     // distill_live
-constexpr int kMostLiveBlocks = 256;  // of all ranks together
+constexpr int kMostParts = 256;       // blocks of distill_teacher, all ranks together
 constexpr int kMostSplits = 64;       // blocks to a token
 constexpr float kLn2 = 0.69314718f;
+constexpr float kNoEntry = -1.0f;
 
 struct DistillArgs {
     RowPtrs z, teacher, index, dz;
     VecPtrs weight, row_loss;
-    int64_t rows[DDP_MAX_RANKS];
-    int64_t first[DDP_MAX_RANKS];   // tokens of the ranks before
-    int64_t tokens;
+    int64_t rows[kGroup];
+    int64_t first[kGroup];          // tokens of the ranks before, of all of the call
+    int64_t tokens;                 // of all ranks
     int64_t vocab;
     int64_t seg;                    // logits of a split (distill_part, distill_emit)
-    int32_t n_ranks, top, splits;
+    int32_t n_ranks;                // of this launch
+    int32_t top, splits;
     int tdt, index_bytes;
     float tau, scale;               // scale: grad_scale * n_ranks * tau
     float inv_tau, exp_scale;       // 1 / tau, log2(e) / tau
     float far;                      // logits up to this times exp_scale are finite
-    int32_t live_blocks;            // parts of `den`
-    float *den;                     // [live_blocks] parts of D
+    int32_t parts;                  // of `den`
+    float *den;                     // [parts] parts of D
+    float *den_out;                 // where this launch's ranks have theirs (distill_teacher)
     float *w;                       // [tokens] the weight of each live token, 0 for others
-    float *loss_of;                 // [tokens] row_loss; split rows: its part without m and s
+    float *loss_of;                 // [tokens] row_loss; before: the teacher's part of it
     float *ref;                     // [tokens] split rows: r
     float *part;                    // [tokens][splits] pairs (m, s)
+    float *prob;                    // [tokens][top] what the gradient takes off at an entry's
+                                    // place (distill_teacher), kNoEntry where nothing
     float *loss;
 };
 
@@ -258,15 +263,6 @@ __device__ __forceinline__ void join_centres(const float *ms, const float *ss, i
     join_by(ms, ss, waves, m, s, [](float d) { return __builtin_amdgcn_exp2f(d); });
 }
 
-// D, from its parts: every lane of a wave gets it.
-__device__ __forceinline__ float total_weight(const DistillArgs &a)
-{
-    float d = 0.0f;
-#pragma unroll 1
-    for (uint32_t b = threadIdx.x % kWave; b < (uint32_t)a.live_blocks; b += kWave) d += a.den[b];
-    return wave_all<OpSum>(d);
-}
-
 // dz at the entries' places within [lo, hi): every thread its own entries.  An
 // entry of an index named several times has the sum of their p, in their
 // order, so all of them store the same value.
@@ -309,34 +305,201 @@ __device__ __forceinline__ void note_row(const DistillArgs &a, int r, int64_t ro
     if (a.row_loss.p[r]) st_elem<float>(a.row_loss.p[r], row, loss);
 }
 
-// ---------------------------------------------------------------- D
+// ---------------------------------------------------------------- the teacher
 
-// D in parts, one to a block: each wave takes tokens in turn, its lanes the
-// token's entries.  (The gradient needs D before the first row is written;
-// the loss alone takes it from the rows' own weights.)
-__global__ void __launch_bounds__(kLiveThreads) distill_live(DistillArgs a)
+// Ahead of the gradient of many tokens, a wave to a token: its weight (0 unless
+// live), E = sum p log p, and for each entry what the gradient takes off at its
+// place.  Of entries that name the same index the first has the sum of their p
+// and the others nothing, so every place is stored once.  Each block also sums
+// its tokens' weights into a part of D, which the first row's gradient needs.
+//
+// Indices that occur twice are found by a table of 32 bits to an entry, hashed by
+// the index: an entry that finds its bit set is suspect (one in 64 by chance, at
+// most), and only for suspects are all the entries compared.  What a group of
+// equal indices gets does not depend on which of them was suspected.
+constexpr int kTeacherWords = 3;   // LDS words to an entry: place, p, bits
+
+__global__ void __launch_bounds__(kMostWaves * kWave) distill_teacher(DistillArgs a)
 {
-    __shared__ float lds[kLiveThreads / kWave];
-    const int r = blockIdx.y, l = threadIdx.x % kWave;
-    const int64_t step = (int64_t)gridDim.x * (kLiveThreads / kWave);
+    extern __shared__ __align__(16) int32_t entry_words[];
+    __shared__ float lds[kMostWaves];
+    const int r = blockIdx.y, l = threadIdx.x % kWave, wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
+    const int padded = padded_top(a.top);
+    int32_t *at = entry_words + wave * padded * kTeacherWords;
+    float *prob = reinterpret_cast<float *>(at + padded);
+    uint32_t *bits = reinterpret_cast<uint32_t *>(at + 2 * padded);
+    const int64_t step = (int64_t)gridDim.x * waves;
     float d = 0.0f;
-    for (int64_t row = (int64_t)blockIdx.x * (kLiveThreads / kWave) + threadIdx.x / kWave; row < a.rows[r];
-         row += step) {
-        const float w = weight_of(a, r, row);
-        if (w == 0.0f) continue;
+    for (int64_t row = (int64_t)blockIdx.x * waves + wave; row < a.rows[r]; row += step) {
+        const int64_t token = a.first[r] + row;
         const char *index = a.index.p[r] + row * a.index.pitch;
         const char *teacher = a.teacher.p[r] + row * a.teacher.pitch;
-        bool live = false;
-        for (int k = l; k - l < a.top && !live; k += kWave) {
-            float t;
-            live = __any(k < a.top && entry_of(a, index, teacher, k, &t) >= 0);
+        float tm = -INFINITY;
+        for (int k = l; k < padded; k += kWave) {
+            float t = 0.0f;
+            const int32_t j = k < a.top ? entry_of(a, index, teacher, k, &t) : -1;
+            at[k] = j;
+            prob[k] = t;
+            bits[k] = 0;
+            if (j >= 0) tm = fmaxf(tm, t);
         }
-        if (live) d += w;
+        const float w = weight_of(a, r, row);
+        tm = wave_all<OpMax>(tm);
+        if (w == 0.0f || tm == -INFINITY) {
+            if (l == 0) a.w[token] = 0.0f;
+            continue;
+        }
+        d += w;
+        float mass = 0.0f;
+        for (int k = l; k < padded; k += kWave) {
+            const float e = at[k] >= 0 ? exp_of(a, prob[k] - tm) : 0.0f;
+            prob[k] = e;
+            mass += e;
+        }
+        const float inv = 1.0f / wave_all<OpSum>(mass);
+        float ent = 0.0f;
+        float *out = a.prob + token * a.top;
+        for (int k = l; k < padded; k += kWave) {
+            const float p = prob[k] * inv;
+            prob[k] = p;
+            if (p > 0.0f || p != p) ent += p * logf(p);
+            if (k < a.top) out[k] = at[k] >= 0 ? p : kNoEntry;
+        }
+        ent = wave_all<OpSum>(ent);
+        if (l == 0) {
+            a.w[token] = w;
+            a.loss_of[token] = ent;
+        }
+        for (int k0 = 0; k0 < a.top; k0 += kWave) {
+            const int32_t mine = k0 + l < a.top ? at[k0 + l] : -1;
+            bool suspect = false;
+            if (mine >= 0) {
+                const uint32_t h = (uint32_t)mine * 0x9E3779B1u;
+                const uint32_t bit = 1u << (h >> 27);
+                suspect = atomicOr(&bits[((h & 0x7ffffffu) * (uint64_t)(uint32_t)padded) >> 27], bit) & bit;
+            }
+            uint64_t todo = __ballot(suspect);
+            while (todo) {
+                const int32_t j = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
+                todo &= todo - 1;
+                float p = 0.0f;
+                int first = -1;
+                for (int i0 = 0; i0 < a.top; i0 += kWave) {
+                    const bool same = i0 + l < a.top && at[i0 + l] == j;
+                    if (same) p += prob[i0 + l];
+                    const uint64_t any = __ballot(same);
+                    if (any && first < 0) first = i0 + __builtin_ctzll(any);
+                }
+                p = wave_all<OpSum>(p);
+                for (int i = l; i < a.top; i += kWave)
+                    if (at[i] == j) out[i] = i == first ? p : kNoEntry;
+            }
+        }
     }
     d = l == 0 ? d : 0.0f;
-    d = block_all<OpSum>(d, lds, kLiveThreads / kWave);
-    if (threadIdx.x == 0) a.den[blockIdx.y * gridDim.x + blockIdx.x] = d;
+    d = block_all<OpSum>(d, lds, waves);
+    if (threadIdx.x == 0) a.den_out[blockIdx.y * gridDim.x + blockIdx.x] = d;
 }
+
+// The entries of a token as distill_teacher left them, in the gradient's
+// kernels: each thread's first one is loaded ahead of the logits, and goes to
+// LDS when the student's logit there is asked for (raw words that nothing waits
+// for); the rest follow, before the first store.
+struct Marks {
+    uint32_t at, z;
+    float p;
+    __device__ __forceinline__ void load(const DistillArgs &a, int r, int64_t row, int64_t token)
+    {
+        if ((int)threadIdx.x < a.top) {
+            at = ld_elem<uint32_t>(a.index.p[r] + row * a.index.pitch + (int)threadIdx.x * a.index_bytes, 0);
+            p = a.prob[token * a.top + (int)threadIdx.x];
+        }
+    }
+    template <int DT>
+    __device__ __forceinline__ void gather(const DistillArgs &a, const char *row_z, const Entries &en)
+    {
+        if ((int)threadIdx.x < a.top) {
+            const uint32_t j = p == kNoEntry ? 0u : at;
+            z = DT == kF32 ? ld_elem<uint32_t>(row_z, j) : (uint32_t)ld_elem<uint16_t>(row_z, j);
+            en.at[threadIdx.x] = (int32_t)at;
+            en.prob[threadIdx.x] = p;
+        }
+    }
+    template <int DT>
+    __device__ __forceinline__ void stash(const DistillArgs &a, int r, int64_t row, int64_t token,
+                                          const char *row_z, const Entries &en) const
+    {
+        if ((int)threadIdx.x < a.top) en.z[threadIdx.x] = __uint_as_float(DT == kF32 ? z : z << 16);
+#pragma unroll 1
+        for (int k = threadIdx.x + blockDim.x; k < a.top; k += blockDim.x) {
+            const uint32_t j = ld_elem<uint32_t>(a.index.p[r] + row * a.index.pitch + k * a.index_bytes, 0);
+            const float q = a.prob[token * a.top + k];
+            en.at[k] = (int32_t)j;
+            en.prob[k] = q;
+            en.z[k] = load_elem<DT>(row_z, q == kNoEntry ? 0 : (int64_t)j);
+        }
+    }
+};
+
+// What the waves of a block exchange in the gradient's kernels.
+struct Exchange {
+    float ms[kMostWaves], ss[kMostWaves];   // their pairs
+    float dot[kMostWaves];                  // their parts of sum p (z - m) / tau
+    float den;                              // D
+};
+__device__ __forceinline__ void put_pair(Exchange &x, float m, float s)
+{
+    if (threadIdx.x % kWave == 0) {
+        x.ms[threadIdx.x / kWave] = m;
+        x.ss[threadIdx.x / kWave] = s;
+    }
+}
+// D into LDS, by the block's last wave.
+__device__ __forceinline__ void put_den(const DistillArgs &a, Exchange &x)
+{
+    if (threadIdx.x < blockDim.x - kWave) return;
+    float d = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kMostParts / kWave; ++e) {
+        const int b = e * kWave + (int)threadIdx.x % kWave;
+        if (b < a.parts) d += a.den[b];
+    }
+    d = wave_all<OpSum>(d);
+    if (threadIdx.x % kWave == 0) x.den = d;
+}
+// This wave's part of sum p d(z), d the logit below the row's largest.
+template <class Below>
+__device__ __forceinline__ void put_dot(const DistillArgs &a, Exchange &x, const Entries &en, Below &&below)
+{
+    float t = 0.0f;
+    for (int k = threadIdx.x; k < a.top; k += blockDim.x) {
+        const float p = en.prob[k];
+        if (p > 0.0f || p != p) t += p * below(en.z[k]);
+    }
+    t = wave_all<OpSum>(t);
+    if (threadIdx.x % kWave == 0) x.dot[threadIdx.x / kWave] = t;
+}
+// Past the barrier that ends the stores: the entries' places again, and the row's
+// loss.  unit: of the dot, in natural logarithms.
+template <int DT, class Exp>
+__device__ __forceinline__ void emit_marks(const DistillArgs &a, int r, int64_t row, float w, const Exchange &x,
+                                           const Entries &en, char *dz, Exp &&exp_z, float s, float c, float unit)
+{
+    for (int k = threadIdx.x; k < a.top; k += blockDim.x) {
+        const float p = en.prob[k];
+        if (p == kNoEntry) continue;
+        store_elem<DT>(dz, en.at[k], c * (exp_z(en.z[k]) * (1.0f / s) - p));
+    }
+    if (threadIdx.x < kWave) {
+        const float dot = join_waves<OpSum>(x.dot, blockDim.x / kWave, 0.0f);
+        if (threadIdx.x == 0) {
+            const float ent = a.loss_of[a.first[r] + row];
+            note_row(a, r, row, w, a.tau * a.tau * (ent - unit * dot + logf(s)));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- the loss
 
 // loss = sum of w row / sum of w, by one block.  With splits the rows' parts
 // are joined here first.
@@ -354,9 +517,10 @@ __device__ void finish(const DistillArgs &a, float *lds)
             for (int k = 0; k < a.splits; ++k) m = fmaxf(m, part[2 * k]);
             for (int k = 0; k < a.splits; ++k) s += part[2 * k + 1] * exp_of(a, part[2 * k] - m);
             loss = a.tau * a.tau * (loss + ((m - a.ref[i]) * a.inv_tau + logf(s)));
-            int r = 0;
-            while (i >= a.first[r] + a.rows[r]) ++r;
-            if (a.row_loss.p[r]) st_elem<float>(a.row_loss.p[r], i - a.first[r], loss);
+            // the losses of this launch's ranks (every launch adds up all tokens)
+            for (int r = 0; r < a.n_ranks; ++r)
+                if (a.row_loss.p[r] && i >= a.first[r] && i < a.first[r] + a.rows[r])
+                    st_elem<float>(a.row_loss.p[r], i - a.first[r], loss);
         }
         d += w;
         l += w * loss;
@@ -374,37 +538,6 @@ __global__ void __launch_bounds__(kFarThreads) distill_total(DistillArgs a)
 
 // ---------------------------------------------------------------- a block to a token
 
-// What the waves of a block tell one another: their pairs, and what the first
-// knows of the teacher.
-struct Exchange {
-    float ms[kMostWaves], ss[kMostWaves];
-    float ref, base, den;
-    int alive;
-};
-
-// The block's first wave, past its share of the logits: the teacher.
-template <int DT, bool GRAD>
-__device__ __forceinline__ void teacher_wave(const DistillArgs &a, int r, int64_t row, const char *z, const Entries &en,
-                                             const FirstEntry &first, Exchange &x)
-{
-    const bool live = teacher_of<DT>(a, r, row, en, first, z, 0, a.vocab);
-    float ref;
-    const float base = divergence_of(a, en, &ref);
-    const float d = GRAD ? total_weight(a) : 0.0f;
-    if (threadIdx.x == 0) {
-        x.alive = live;
-        x.ref = ref;
-        x.base = base;
-        x.den = d;
-    }
-}
-__device__ __forceinline__ void data_wave(Exchange &x, float m, float s)
-{
-    if (threadIdx.x % kWave == 0) {
-        x.ms[threadIdx.x / kWave] = m;
-        x.ss[threadIdx.x / kWave] = s;
-    }
-}
 // 2^(z k - c) with k = log2(e) / tau, one fused multiply-add to a logit.  c
 // stands for the largest logit m: c = fl(k m) with m within [-far, far], where
 // k far is finite.  The same c is taken out of every sum again, so its rounding
@@ -422,13 +555,24 @@ __device__ __forceinline__ float exp_at(const DistillArgs &a, float z, float c)
 // through exp((z - m) / tau) with the subtraction first.
 __device__ __forceinline__ bool sane(float s) { return s >= FLT_MIN && s <= FLT_MAX; }
 
+// Elements by which bf16 rows start past a 4-byte boundary.  16-byte accesses
+// off one take 35 % longer (4 x 512 x 50257: 61 us, x 50264: 45), so the vectors
+// of a row start on one: the first element of an odd row is taken by itself,
+// with the last few that fill no vector.
+template <int DT>
+__device__ __forceinline__ int odd_start(const char *row)
+{
+    return DT == kBF16 ? (int)(reinterpret_cast<uintptr_t>(row) >> 1 & 1) : 0;
+}
+
 // The pair of this thread's share of the n logits at z, the block's threads
 // taking U vectors each to a step: (m, s), or with FAST (c, s) of exp_at.
-template <int DT, bool FAST>
+template <int DT, bool FAST, bool NT>
 __device__ __forceinline__ void stats_of(const DistillArgs &a, const char *z, int64_t n, float *first, float *s)
 {
     constexpr int V = kVec<DT>, U = 4;
-    const int64_t step = (int64_t)blockDim.x * 16, vecs = n / V;
+    const int head = (int)min64(odd_start<DT>(z), n);
+    const int64_t step = (int64_t)blockDim.x * 16, vecs = (n - head) / V;
     const uint32_t off = threadIdx.x * 16;
     float own = -FLT_MAX, mark = FAST ? centre_of(a, -FLT_MAX) : own, sum = 0.0f;
     auto add = [&](const u32x4 *v, int cnt) {
@@ -447,12 +591,12 @@ __device__ __forceinline__ void stats_of(const DistillArgs &a, const char *z, in
                 sum += FAST ? exp_at(a, x, to) : exp_of(a, x - to);
             }
     };
-    const char *p = z;
+    const char *p = z + head * kSize<DT>;
     int64_t left = vecs;
     for (; left >= U * (int64_t)blockDim.x; left -= U * (int64_t)blockDim.x, p += U * step) {
         u32x4 v[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) v[i] = ld_vec<false, u32x4>(p + i * step + off);
+        for (int i = 0; i < U; ++i) v[i] = ld_vec<NT, u32x4>(p + i * step + off);
         add(v, U);
     }
     if (left > 0) {   // vectors past the end: one before it, with exp = 0 in its place
@@ -460,7 +604,7 @@ __device__ __forceinline__ void stats_of(const DistillArgs &a, const char *z, in
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int64_t k = i * (int64_t)blockDim.x + threadIdx.x;
-            v[i] = ld_vec<false, u32x4>(p + min64(k, left - 1) * 16);
+            v[i] = ld_vec<NT, u32x4>(p + min64(k, left - 1) * 16);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -470,9 +614,8 @@ __device__ __forceinline__ void stats_of(const DistillArgs &a, const char *z, in
             }
         add(v, U);
     }
-    const int64_t j = vecs * V + threadIdx.x;   // fewer than V are left
-    if (j < n) {
-        const float x = load_elem<DT>(z, j);
+    if ((int)threadIdx.x < n - vecs * V) {   // the elements in no vector
+        const float x = load_elem<DT>(z, (int)threadIdx.x < head ? 0 : vecs * V + threadIdx.x);
         own = fmaxf(own, x);
         const float to = FAST ? centre_of(a, own) : own;
         sum = FAST ? sum * __builtin_amdgcn_exp2f(mark - to) + exp_at(a, x, to)
@@ -484,13 +627,14 @@ __device__ __forceinline__ void stats_of(const DistillArgs &a, const char *z, in
 }
 
 // dz of the n logits at z, entries aside: f exp_z(z).  The logits may lie where
-// dz does, so the last few are taken by element.
+// dz does, so no element is read by another thread than its writer.
 template <int DT, class Exp>
 __device__ __forceinline__ void emit_of(const char *z, char *dz, int64_t n, float f, Exp &&exp_z)
 {
     constexpr int V = kVec<DT>, U = 2;
-    const int64_t step = (int64_t)blockDim.x * 16, vecs = n / V;
-    const uint32_t off = threadIdx.x * 16;
+    const int head = (int)min64(odd_start<DT>(dz), n);
+    const int64_t step = (int64_t)blockDim.x * 16, vecs = (n - head) / V;
+    const uint32_t off = threadIdx.x * 16 + head * kSize<DT>;
     auto put = [&](const u32x4 &v, char *to) {
         float y[V];
 #pragma unroll
@@ -505,57 +649,103 @@ __device__ __forceinline__ void emit_of(const char *z, char *dz, int64_t n, floa
 #pragma unroll
         for (int i = 0; i < U; ++i) put(v[i], dz + at + i * step + off);
     }
-    for (int64_t k = threadIdx.x; k < left; k += blockDim.x)
-        put(ld_vec<false, u32x4>(z + at + k * 16), dz + at + k * 16);
-    const int64_t j = vecs * V + threadIdx.x;
-    if (j < n) store_elem<DT>(dz, j, exp_z(load_elem<DT>(z, j)) * f);
+    for (int64_t k = threadIdx.x; k < left; k += blockDim.x) {
+        const int64_t o = at + k * 16 + head * kSize<DT>;
+        put(ld_vec<false, u32x4>(z + o), dz + o);
+    }
+    if ((int)threadIdx.x < n - vecs * V) {
+        const int64_t j = (int)threadIdx.x < head ? 0 : vecs * V + threadIdx.x;
+        store_elem<DT>(dz, j, exp_z(load_elem<DT>(z, j)) * f);
+    }
 }
 
-// The token's loss and, with GRAD, its gradient by a block of `waves` waves, the
-// row read from memory: once for the loss, once more for the gradient.  The
-// teacher is looked up by the first wave unless `known`.
-template <int DT, bool GRAD, bool FAST>
-__device__ __forceinline__ bool row_far(const DistillArgs &a, int r, int64_t row, float w, const char *z, char *dz,
-                                        const Entries &en, Exchange &x, bool known)
+// The loss of a token by a block, its row read once.
+template <int DT, bool FAST>
+__device__ __forceinline__ bool loss_of_row(const DistillArgs &a, int r, int64_t row, float w, const char *z,
+                                            const Entries &en, float *pairs)
 {
     const int waves = blockDim.x / kWave;
     FirstEntry first;
-    const bool look = threadIdx.x < kWave && !known;
+    const bool look = threadIdx.x < kWave;
     if (look) first.load(a, r, row);
     float m, s;
-    stats_of<DT, FAST>(a, z, a.vocab, &m, &s);
+    stats_of<DT, FAST, true>(a, z, a.vocab, &m, &s);
+    bool live = false;
+    float ref = 0.0f, base = 0.0f;
     if (look) {
         first.gather<DT>(a, z, 0, a.vocab);
-        teacher_wave<DT, GRAD>(a, r, row, z, en, first, x);
+        live = teacher_of<DT>(a, r, row, en, first, z, 0, a.vocab);
+        base = divergence_of(a, en, &ref);
     }
     wave_join<FAST>(a, &m, &s);
-    data_wave(x, m, s);
+    if (threadIdx.x % kWave == 0) {
+        pairs[threadIdx.x / kWave] = m;
+        pairs[kMostWaves + threadIdx.x / kWave] = s;
+    }
     __syncthreads();
     if (FAST)
-        join_centres(x.ms, x.ss, waves, &m, &s);
+        join_centres(pairs, pairs + kMostWaves, waves, &m, &s);
     else
-        join_pairs(a, x.ms, x.ss, waves, &m, &s);
+        join_pairs(a, pairs, pairs + kMostWaves, waves, &m, &s);
     if (FAST && !sane(s)) return false;
-    const bool live = x.alive != 0;
     if (threadIdx.x == 0) {
         // the row's largest logit over tau above r / tau, the product with r exact inside the fma
-        const float up = FAST ? kLn2 * __builtin_fmaf(-x.ref, a.exp_scale, m) : (m - x.ref) * a.inv_tau;
-        note_row(a, r, row, live ? w : 0.0f, live ? a.tau * a.tau * (x.base + (up + logf(s))) : 0.0f);
+        const float up = FAST ? kLn2 * __builtin_fmaf(-ref, a.exp_scale, m) : (m - ref) * a.inv_tau;
+        note_row(a, r, row, live ? w : 0.0f, live ? a.tau * a.tau * (base + (up + logf(s))) : 0.0f);
     }
-    if (!GRAD) return true;
-    if (!live) {
-        emit_zeros<DT>(dz, 0, a.vocab);
-        return true;
-    }
-    const float c = a.scale * (w / x.den), inv_s = 1.0f / s;
-    auto exp_z = [&](float q) { return FAST ? exp_at(a, q, m) : exp_of(a, q - m); };
-    emit_of<DT>(z, dz, a.vocab, inv_s * c, exp_z);
-    __syncthreads();   // the entries' places are stored again
-    emit_entries<DT>(a, en, dz, exp_z, inv_s, c, 0, a.vocab);
     return true;
 }
 
-template <int DT, bool GRAD>
+template <int DT>
+__global__ void __launch_bounds__(kLossThreads) distill_row(DistillArgs a, int64_t first_row)
+{
+    const Entries en = entries_of(a);
+    __shared__ float pairs[2 * kMostWaves];
+    const int r = blockIdx.y;
+    if (first_row + blockIdx.x >= a.rows[r]) return;
+    const int64_t row = row_of_block(first_row + blockIdx.x, a.rows[r]);
+    const float w = weight_of(a, r, row);
+    if (w == 0.0f) {
+        if (threadIdx.x == 0) note_row(a, r, row, 0.0f, 0.0f);
+        return;
+    }
+    const char *z = a.z.p[r] + row * a.z.pitch;
+    if (loss_of_row<DT, true>(a, r, row, w, z, en, pairs)) return;
+    __syncthreads();
+    loss_of_row<DT, false>(a, r, row, w, z, en, pairs);
+}
+
+// The gradient of a token by a block, its row read twice.
+template <int DT, bool FAST>
+__device__ __forceinline__ bool grad_of_row(const DistillArgs &a, int r, int64_t row, float w, const char *z, char *dz,
+                                            const Entries &en, Exchange &x)
+{
+    const int64_t token = a.first[r] + row;
+    Marks mk;
+    mk.load(a, r, row, token);
+    float m, s;
+    stats_of<DT, FAST, false>(a, z, a.vocab, &m, &s);
+    mk.gather<DT>(a, z, en);
+    mk.stash<DT>(a, r, row, token, z, en);
+    put_den(a, x);
+    wave_join<FAST>(a, &m, &s);
+    put_pair(x, m, s);
+    __syncthreads();
+    if (FAST)
+        join_centres(x.ms, x.ss, blockDim.x / kWave, &m, &s);
+    else
+        join_pairs(a, x.ms, x.ss, blockDim.x / kWave, &m, &s);
+    if (FAST && !sane(s)) return false;
+    const float c = a.scale * (w / x.den);
+    auto exp_z = [&](float q) { return FAST ? exp_at(a, q, m) : exp_of(a, q - m); };
+    put_dot(a, x, en, [&](float q) { return FAST ? __builtin_fmaf(q, a.exp_scale, -m) : (q - m) * a.inv_tau; });
+    emit_of<DT>(z, dz, a.vocab, c / s, exp_z);
+    __syncthreads();   // the entries' places are stored again
+    emit_marks<DT>(a, r, row, w, x, en, dz, exp_z, s, c, FAST ? kLn2 : 1.0f);
+    return true;
+}
+
+template <int DT>
 __global__ void __launch_bounds__(kFarThreads) distill_far(DistillArgs a, int64_t first_row)
 {
     const Entries en = entries_of(a);
@@ -563,17 +753,17 @@ __global__ void __launch_bounds__(kFarThreads) distill_far(DistillArgs a, int64_
     const int r = blockIdx.y;
     if (first_row + blockIdx.x >= a.rows[r]) return;
     const int64_t row = row_of_block(first_row + blockIdx.x, a.rows[r]);
-    const float w = weight_of(a, r, row);
-    char *dz = GRAD ? a.dz.p[r] + row * a.dz.pitch : nullptr;
+    const float w = a.w[a.first[r] + row];
+    char *dz = a.dz.p[r] + row * a.dz.pitch;
     if (w == 0.0f) {
         if (threadIdx.x == 0) note_row(a, r, row, 0.0f, 0.0f);
-        if (GRAD) emit_zeros<DT>(dz, 0, a.vocab);
+        emit_zeros<DT>(dz, 0, a.vocab);
         return;
     }
     const char *z = a.z.p[r] + row * a.z.pitch;
-    if (row_far<DT, GRAD, true>(a, r, row, w, z, dz, en, x, false)) return;
+    if (grad_of_row<DT, true>(a, r, row, w, z, dz, en, x)) return;
     __syncthreads();
-    row_far<DT, GRAD, false>(a, r, row, w, z, dz, en, x, true);
+    grad_of_row<DT, false>(a, r, row, w, z, dz, en, x);
 }
 
 // What follows takes the vectors' elements apart anew: kept apart from one use
@@ -587,19 +777,24 @@ __device__ __forceinline__ void again(u32x4 (&v)[NV])
 
 // The gradient with the row in registers, NV 16-byte vectors to a thread: f32
 // holds the exponentials, bf16 the packed logits (half the registers, so twice
-// the rows on a CU) and takes each exponential twice.
+// the rows on a CU) and takes each exponential twice.  Vector k starts at
+// element 8 k - head (odd_start) but for the first and the last, which are moved
+// inside the row: they share elements with their neighbours, all of them load
+// before the barrier, and a sum counts an element for the vector whose place
+// it is.  bf16 stores the same values from both; f32 stores the last vector's own
+// elements alone.
 template <int DT, int NV, bool NT>
-__global__ void __launch_bounds__(kMostWaves * kWave) __attribute__((amdgpu_waves_per_eu(4)))
-distill_held(DistillArgs a, int64_t first_row)
+__global__ void __launch_bounds__(kMostWaves * kWave) distill_held(DistillArgs a, int64_t first_row)
 {
     constexpr int V = kVec<DT>, size = kSize<DT>;
-    constexpr int U = DT == kF32 ? NV : 2;   // vectors to a step of the running pair
+    constexpr int U = DT == kF32 ? NV : 1;   // vectors to a step of the running pair
     const Entries en = entries_of(a);
     __shared__ Exchange x;
     const int r = blockIdx.y, threads = blockDim.x, waves = threads / kWave;
     if (first_row + blockIdx.x >= a.rows[r]) return;
     const int64_t row = row_of_block(first_row + blockIdx.x, a.rows[r]);
-    const float w = weight_of(a, r, row);
+    const int64_t token = a.first[r] + row;
+    const float w = a.w[token];
     char *dz = a.dz.p[r] + row * a.dz.pitch;
     if (w == 0.0f) {
         if (threadIdx.x == 0) note_row(a, r, row, 0.0f, 0.0f);
@@ -607,15 +802,17 @@ distill_held(DistillArgs a, int64_t first_row)
         return;
     }
     const char *z = a.z.p[r] + row * a.z.pitch;
-    const int n = (int)a.vocab;
-    FirstEntry first;
-    if (threadIdx.x < kWave) first.load(a, r, row);
+    const int n = (int)a.vocab, shift = odd_start<DT>(z) ? V - 1 : 0;
+    Marks mk;
+    mk.load(a, r, row, token);
+    auto place = [&](int k) { return k * V - shift; };
+    auto inside = [&](int j) { return max(0, min(j, n - V)); };
     u32x4 v[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        v[i] = ld_vec<NT, u32x4>(z + piece_of<V>(i * threads + (int)threadIdx.x, n).at * size);
-    if (threadIdx.x < kWave) first.gather<DT>(a, z, 0, n);
-    const int wave_end = __builtin_amdgcn_readfirstlane(((int)threadIdx.x | (kWave - 1)) + 1);
+        v[i] = ld_vec<true, u32x4>(z + (uint32_t)inside(place(i * threads + (int)threadIdx.x)) * size);
+    mk.gather<DT>(a, z, en);
+    const int wave0 = __builtin_amdgcn_readfirstlane((int)threadIdx.x & ~(kWave - 1));
     float own = -FLT_MAX, s = 0.0f, c_own = 0.0f;
 #pragma unroll
     for (int g = 0; g < NV; g += U) {
@@ -634,13 +831,14 @@ distill_held(DistillArgs a, int64_t first_row)
                 ex[e] = exp_at(a, value<V, DT>(v[i], e), c);
                 t += ex[e];
             }
-            if ((i * threads + wave_end) * V > n) {   // this wave's vectors reach the row's end
+            // a wave with a vector of the row's start or end counts by element
+            if (place(i * threads + wave0 + kWave) > n || place(i * threads + wave0) < 0) {
                 int t0 = threadIdx.x;
                 asm volatile("" : "+v"(t0));
-                const int skip = (int)piece_of<V>(i * threads + t0, n).skip;
+                const int j = place(i * threads + t0), d = j - inside(j);
                 t = 0.0f;
 #pragma unroll
-                for (int e = 0; e < V; ++e) t += e >= skip ? ex[e] : 0.0f;
+                for (int e = 0; e < V; ++e) t += (uint32_t)(e - d) < (uint32_t)V ? ex[e] : 0.0f;
             }
             s += t;
             if (DT == kF32) {   // in place of the logits
@@ -649,28 +847,21 @@ distill_held(DistillArgs a, int64_t first_row)
             }
         }
     }
-    if (threadIdx.x < kWave) teacher_wave<DT, true>(a, r, row, z, en, first, x);
+    mk.stash<DT>(a, r, row, token, z, en);
+    put_den(a, x);
     float c_row = c_own, s_row = s;
     wave_join<true>(a, &c_row, &s_row);
-    data_wave(x, c_row, s_row);
+    put_pair(x, c_row, s_row);
     __syncthreads();
     join_centres(x.ms, x.ss, waves, &c_row, &s_row);
     if (!sane(s_row)) {   // once more, from the row as it still lies in memory
         __syncthreads();
-        row_far<DT, true, false>(a, r, row, w, z, dz, en, x, true);
+        grad_of_row<DT, false>(a, r, row, w, z, dz, en, x);
         return;
     }
-    const bool live = x.alive != 0;
-    if (threadIdx.x == 0) {
-        const float up = kLn2 * __builtin_fmaf(-x.ref, a.exp_scale, c_row);
-        note_row(a, r, row, live ? w : 0.0f, live ? a.tau * a.tau * (x.base + (up + logf(s_row))) : 0.0f);
-    }
-    if (!live) {
-        emit_zeros<DT>(dz, 0, a.vocab);
-        return;
-    }
-    const float c = a.scale * (w / x.den), inv_s = 1.0f / s_row;
-    const float f = DT == kF32 ? __builtin_amdgcn_exp2f(c_own - c_row) * inv_s * c : inv_s * c;
+    const float c = a.scale * (w / x.den);
+    put_dot(a, x, en, [&](float q) { return __builtin_fmaf(q, a.exp_scale, -c_row); });
+    const float f = DT == kF32 ? __builtin_amdgcn_exp2f(c_own - c_row) * (c / s_row) : c / s_row;
     int t0 = threadIdx.x;
     asm volatile("" : "+v"(t0));   // the vectors' places are found anew, not kept in registers
     if (DT == kBF16) again(v);
@@ -680,11 +871,17 @@ distill_held(DistillArgs a, int64_t first_row)
 #pragma unroll
         for (int e = 0; e < V; ++e)
             y[e] = (DT == kF32 ? value<V, DT>(v[i], e) : exp_at(a, value<V, DT>(v[i], e), c_row)) * f;
-        const Piece pc = piece_of<V>(i * threads + t0, n);
-        if (owned<V>(pc)) st_values<V, DT, NT>(dz + pc.at * size, y);
+        const int j = place(i * threads + t0), at = inside(j);
+        if (DT == kF32 && j != at) {   // its neighbour's exponentials are against another centre
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (at + e >= j) store_elem<DT>(dz, at + e, y[e]);
+        } else if (j < n) {
+            st_values<V, DT, NT>(dz + (uint32_t)at * size, y);
+        }
     }
     __syncthreads();   // the entries' places are stored again
-    emit_entries<DT>(a, en, dz, [&](float q) { return exp_at(a, q, c_row); }, inv_s, c, 0, n);
+    emit_marks<DT>(a, r, row, w, x, en, dz, [&](float q) { return exp_at(a, q, c_row); }, s_row, c, kLn2);
 }
 
 // ---------------------------------------------------------------- several blocks to a token
@@ -711,7 +908,7 @@ __global__ void __launch_bounds__(kPartThreads) distill_part(DistillArgs a)
     FirstEntry first;
     const bool look = split == 0 && threadIdx.x < kWave;
     if (look) first.load(a, r, row);
-    stats_of<DT, false>(a, z + lo * kSize<DT>, hi - lo, &m, &s);
+    stats_of<DT, false, false>(a, z + lo * kSize<DT>, hi - lo, &m, &s);
     wave_join<false>(a, &m, &s);
     if (threadIdx.x % kWave == 0) {
         ms[threadIdx.x / kWave] = m;
@@ -800,13 +997,22 @@ Splits splits_of(int64_t tokens, int64_t vocab)
     return {(int32_t)n, seg};
 }
 
-int64_t distill_bytes(int64_t tokens, int64_t vocab)
+int64_t distill_bytes(int64_t tokens, int64_t vocab, int64_t top)
 {
-    const int64_t floats = kMostLiveBlocks + 3 * tokens + 2 * tokens * splits_of(tokens, vocab).n;
+    const int64_t n = splits_of(tokens, vocab).n;
+    const int64_t floats = kMostParts + 3 * tokens + (n ? 2 * n : top) * tokens;
     return (floats * 4 + 15) / 16 * 16;
 }
 
 constexpr int64_t kMostThreads = kMostWaves * kWave;
+
+// Bytes moved from which the gradient is stored past the caches (nt): what no
+// longer fits the 256 MB last-level cache.  8 x 512 x 32000 bf16 takes 112 us
+// with nt stores and 123 without, 2 x 255 x 50257 f32 (205 MB) 53 and 50.  The
+// logits are always loaded so: they are read once and no tensor that is to be
+// read again should make room for them (4 x 512 x 50257 bf16: 35 us, 37 without).
+constexpr int64_t kStreamBytes = (int64_t)256 << 20;
+
 
 // Threads of a block that steps through a row of `vecs` vectors, at most `most`.
 int far_threads(int64_t vecs, int most)
@@ -818,9 +1024,10 @@ template <int DT, bool NT>
 ddp_status_t launch_grad(const DistillArgs &a, int64_t most, hipStream_t st)
 {
     constexpr int V = kVec<DT>;
-    const int64_t vecs = (a.vocab + V - 1) / V;
+    const int64_t vecs = (a.vocab + (DT == kBF16 ? V - 1 : 0) + V - 1) / V;   // of a row that starts off a dword
     constexpr int kBig = DT == kF32 ? 16 : 8;   // 64 exponentials to a thread
-    const int nv = a.vocab < V || vecs > kBig * kMostThreads ? 0 : vecs <= 2 * 256 ? 2 : vecs <= kBig / 2 * 256 ? kBig / 2 : kBig;
+    const int nv = a.vocab < V || vecs > kBig * kMostThreads ? 0
+                   : vecs <= 2 * 256 ? 2 : vecs <= kBig / 2 * 256 ? kBig / 2 : kBig;
     const int threads = nv ? (int)((vecs + nv * kWave - 1) / (nv * kWave)) * kWave : far_threads(vecs, kFarThreads);
     const unsigned lds = entry_bytes(a.top);
     return launch_split(most, threads, "distillation kernel launch", [&](int64_t b0, unsigned nb) {
@@ -832,7 +1039,16 @@ ddp_status_t launch_grad(const DistillArgs &a, int64_t most, hipStream_t st)
         else if (nv == kBig)
             distill_held<DT, kBig, NT><<<g, threads, lds, st>>>(a, b0);
         else
-            distill_far<DT, true><<<g, threads, lds, st>>>(a, b0);
+            distill_far<DT><<<g, threads, lds, st>>>(a, b0);
+    });
+}
+
+template <int DT>
+ddp_status_t launch_loss(const DistillArgs &a, int64_t most, hipStream_t st)
+{
+    const int threads = far_threads((a.vocab + kVec<DT> - 1) / kVec<DT>, kLossThreads);
+    return launch_split(most, threads, "distillation kernel launch", [&](int64_t b0, unsigned nb) {
+        distill_row<DT><<<dim3(nb, (unsigned)a.n_ranks), threads, entry_bytes(a.top), st>>>(a, b0);
     });
 }
 
@@ -840,10 +1056,7 @@ template <int DT>
 ddp_status_t launch_rows(const DistillArgs &a, int64_t most, bool grad, bool nt, hipStream_t st)
 {
     if (grad) return nt ? launch_grad<DT, true>(a, most, st) : launch_grad<DT, false>(a, most, st);
-    const int threads = far_threads((a.vocab + kVec<DT> - 1) / kVec<DT>, 256);
-    return launch_split(most, threads, "distillation kernel launch", [&](int64_t b0, unsigned nb) {
-        distill_far<DT, false><<<dim3(nb, (unsigned)a.n_ranks), threads, entry_bytes(a.top), st>>>(a, b0);
-    });
+    return launch_loss<DT>(a, most, st);
 }
 
 ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_t vocab,
@@ -865,7 +1078,7 @@ ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_
     if (total > 0 && (!logits || !logits->rank || !teacher || !teacher->rank || !index ||
                       !index->rank || (grad && (!dlogits || !dlogits->rank))))
         return DDP_ERR_INVALID_ARG;
-    const int64_t need = distill_bytes(total, vocab);
+    const int64_t need = distill_bytes(total, vocab, top);
     if (!workspace || !aligned(workspace, 16)) return DDP_ERR_INVALID_ARG;
     if (workspace_bytes < need) return DDP_ERR_CAPACITY;
     const int esz = dtype_size(dtype), tsz = dtype_size(teacher_dtype);
@@ -885,68 +1098,89 @@ ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_
     op[n++] = span_operand(loss, 1, 4, true);
     op[n++] = span_operand(workspace, need, 1, true);
     if ((st = check_operands(op, n, n_ranks)) != DDP_OK) return st;
-    DistillArgs a;
-    std::memset(&a, 0, sizeof(a));
-    if (total > 0) {
-        set_rows(&a.z, logits, n_ranks, esz);
-        set_rows(&a.teacher, teacher, n_ranks, tsz);
-        set_rows(&a.index, index, n_ranks, index_bytes);
-        set_rows(&a.dz, grad ? dlogits : nullptr, n_ranks, esz);
-        set_vecs(&a.weight, reinterpret_cast<const void *const *>(token_weight), n_ranks);
-        set_vecs(&a.row_loss, reinterpret_cast<const void *const *>(row_loss), n_ranks);
-    }
-    std::memcpy(a.rows, rows, sizeof(int64_t) * (size_t)n_ranks);
-    for (int r = 1; r < n_ranks; ++r) a.first[r] = a.first[r - 1] + rows[r - 1];
     const Splits sp = splits_of(total, vocab);
-    a.tokens = total;
-    a.vocab = vocab;
-    a.seg = sp.seg;
-    a.n_ranks = n_ranks;
-    a.top = top;
-    a.splits = sp.n;
-    a.tdt = teacher_dtype;
-    a.index_bytes = index_bytes;
-    a.tau = temperature;
-    a.scale = grad_scale * (float)n_ranks * temperature;
-    a.inv_tau = 1.0f / temperature;
-    a.exp_scale = (float)(1.4426950408889634 / (double)temperature);   // log2(e) / tau
-    a.far = std::min(0x1p100f, 0x1p120f / a.exp_scale);
-    a.den = static_cast<float *>(workspace);
-    a.w = a.den + kMostLiveBlocks;
-    a.loss_of = a.w + total;
-    a.ref = a.loss_of + total;
-    a.part = a.ref + total;
-    a.loss = loss;
+    DistillArgs all;   // but for the ranks' own
+    std::memset(&all, 0, sizeof(all));
+    all.tokens = total;
+    all.vocab = vocab;
+    all.seg = sp.seg;
+    all.top = top;
+    all.splits = sp.n;
+    all.tdt = teacher_dtype;
+    all.index_bytes = index_bytes;
+    all.tau = temperature;
+    all.scale = grad_scale * (float)n_ranks * temperature;
+    all.inv_tau = 1.0f / temperature;
+    all.exp_scale = (float)(1.4426950408889634 / (double)temperature);   // log2(e) / tau
+    all.far = std::min(0x1p100f, 0x1p120f / all.exp_scale);
+    all.den = static_cast<float *>(workspace);
+    all.w = all.den + kMostParts;
+    all.loss_of = all.w + total;
+    all.ref = all.loss_of + total;
+    all.part = all.prob = all.ref + total;
+    all.loss = loss;
+    // distill_teacher: a wave to a token where there are that many, within 64 KB of LDS to a block
+    const int64_t per_wave = 4 * kTeacherWords * (int64_t)padded_top(top);
+    const int64_t waves = std::min<int64_t>(kMostWaves, 65536 / per_wave);
+    const int64_t blocks =
+        std::max<int64_t>(1, std::min<int64_t>((most + waves - 1) / waves, kMostParts / n_ranks));
+    all.parts = (int32_t)(blocks * n_ranks);
+    int64_t first[DDP_MAX_RANKS] = {0};
+    for (int r = 1; r < n_ranks; ++r) first[r] = first[r - 1] + rows[r - 1];
+    auto group = [&](int32_t r0, int32_t nr) {
+        DistillArgs a = all;
+        set_rows(&a.z, logits, r0, nr, esz);
+        set_rows(&a.teacher, teacher, r0, nr, tsz);
+        set_rows(&a.index, index, r0, nr, index_bytes);
+        set_rows(&a.dz, grad ? dlogits : nullptr, r0, nr, esz);
+        set_vecs(&a.weight, reinterpret_cast<const void *const *>(token_weight), r0, nr);
+        set_vecs(&a.row_loss, reinterpret_cast<const void *const *>(row_loss), r0, nr);
+        std::memcpy(a.rows, rows + r0, sizeof(int64_t) * (size_t)nr);
+        std::memcpy(a.first, first + r0, sizeof(int64_t) * (size_t)nr);
+        a.n_ranks = nr;
+        a.den_out = all.den + r0 * blocks;
+        return a;
+    };
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    if (sp.n) {
-        const dim3 g((unsigned)sp.n, (unsigned)most, (unsigned)n_ranks);
-        if (dtype == DDP_F32)
-            distill_part<kF32><<<g, kPartThreads, entry_bytes(top), hs>>>(a);
-        else
-            distill_part<kBF16><<<g, kPartThreads, entry_bytes(top), hs>>>(a);
-        if ((st = launched("distillation kernel launch")) != DDP_OK) return st;
-        if (grad) {
-            const dim3 e((unsigned)sp.n + 1, (unsigned)most, (unsigned)n_ranks);
+    if (sp.n) {   // several blocks to a token
+        st = for_groups(n_ranks, [&](int32_t r0, int32_t nr) {
+            const dim3 g((unsigned)sp.n, (unsigned)most, (unsigned)nr);
             if (dtype == DDP_F32)
-                distill_emit<kF32><<<e, kPartThreads, entry_bytes(top), hs>>>(a);
+                distill_part<kF32><<<g, kPartThreads, entry_bytes(top), hs>>>(group(r0, nr));
             else
-                distill_emit<kBF16><<<e, kPartThreads, entry_bytes(top), hs>>>(a);
+                distill_part<kBF16><<<g, kPartThreads, entry_bytes(top), hs>>>(group(r0, nr));
+            return launched("distillation kernel launch");
+        });
+        if (st != DDP_OK) return st;
+        return for_groups(n_ranks, [&](int32_t r0, int32_t nr) {
+            const dim3 g((unsigned)sp.n + 1, (unsigned)most, (unsigned)nr);
+            if (!grad)
+                distill_total<<<1, kFarThreads, 0, hs>>>(group(r0, nr));
+            else if (dtype == DDP_F32)
+                distill_emit<kF32><<<g, kPartThreads, entry_bytes(top), hs>>>(group(r0, nr));
+            else
+                distill_emit<kBF16><<<g, kPartThreads, entry_bytes(top), hs>>>(group(r0, nr));
             return launched("distillation gradient kernel launch");
-        }
-    } else if (total > 0) {
+        });
+    }
+    if (total > 0) {
         if (grad) {
-            const int64_t per = kLiveThreads / kWave;
-            const int64_t lb = std::max<int64_t>(1, std::min<int64_t>((most + per - 1) / per,
-                                                                      kMostLiveBlocks / n_ranks));
-            a.live_blocks = (int32_t)(lb * n_ranks);
-            distill_live<<<dim3((unsigned)lb, (unsigned)n_ranks), kLiveThreads, 0, hs>>>(a);
-            if ((st = launched("distillation weight kernel launch")) != DDP_OK) return st;
+            st = for_groups(n_ranks, [&](int32_t r0, int32_t nr) {
+                distill_teacher<<<dim3((unsigned)blocks, (unsigned)nr), (unsigned)(waves * kWave),
+                                  (unsigned)(waves * per_wave), hs>>>(group(r0, nr));
+                return launched("distillation teacher kernel launch");
+            });
+            if (st != DDP_OK) return st;
         }
-        const bool nt = total * vocab * esz * (grad ? 2 : 1) >= (int64_t)256 << 20;
-        st = dtype == DDP_F32 ? launch_rows<kF32>(a, most, grad, nt, hs) : launch_rows<kBF16>(a, most, grad, nt, hs);
+        const bool nt = total * vocab * esz * 2 >= kStreamBytes;
+        st = for_groups(n_ranks, [&](int32_t r0, int32_t nr) {
+            const DistillArgs a = group(r0, nr);
+            if (dtype == DDP_F32) return launch_rows<kF32>(a, most, grad, nt, hs);
+            return launch_rows<kBF16>(a, most, grad, nt, hs);
+        });
         if (st != DDP_OK) return st;
     }
-    distill_total<<<1, kFarThreads, 0, hs>>>(a);
+    distill_total<<<1, kFarThreads, 0, hs>>>(all);
     return launched("distillation total kernel launch");
 }
 
@@ -954,11 +1188,11 @@ ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_
 
 extern "C" {
 
-int64_t ddp_distill_workspace(const int64_t *rows, int32_t n_ranks, int64_t vocab)
+int64_t ddp_distill_workspace(const int64_t *rows, int32_t n_ranks, int64_t vocab, int32_t top)
 {
     int64_t total, most;
-    if (check_shape(rows, n_ranks, vocab, &total, &most) != DDP_OK) return -1;
-    return distill_bytes(total, vocab);
+    if (check_shape(rows, n_ranks, vocab, &total, &most) != DDP_OK || top < 1 || top > DDP_MAX_TOP) return -1;
+    return distill_bytes(total, vocab, top);
 }
 
 ddp_status_t ddp_distill_loss(const int64_t *rows, int32_t n_ranks, int64_t vocab,

@@ -41,7 +41,7 @@ constexpr int64_t kMostGridRows = 1 << 16;   // blocks to a rank of norm_rows, w
 struct NormArgs {
     RowPtrs x, res, sum, y;
     VecPtrs scale;
-    int64_t rows[DDP_MAX_RANKS];
+    int64_t rows[kGroup];
     const char *weight;
     int64_t width;
     int wdt;
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_held(NormArgs a, int6
 
 struct NormGradArgs {
     RowPtrs s, dy, dsum, dx;
-    int64_t rows[DDP_MAX_RANKS];
+    int64_t rows[kGroup];
     const char *weight;
     float *part;        // [n_ranks][blocks][part_width] partial weight gradients, or null
     int64_t width, part_width;   // part_width: width up to a multiple of 8
@@ -621,31 +621,33 @@ ddp_status_t ddp_rms_norm(const int64_t *rows, int32_t n_ranks, int64_t width, c
     if (scale)
         op[n++] = vector_operand(reinterpret_cast<const void *const *>(scale), rows, 1, 4, true);
     if ((st = check_operands(op, n, n_ranks)) != DDP_OK) return st;
-    NormArgs a;
-    std::memset(&a, 0, sizeof(a));
-    set_rows(&a.x, x, n_ranks, esz);
-    set_rows(&a.res, residual, n_ranks, esz);
-    set_rows(&a.sum, sum_out, n_ranks, esz);
-    set_rows(&a.y, y, n_ranks, ysz);
-    set_vecs(&a.scale, reinterpret_cast<const void *const *>(scale), n_ranks);
-    std::memcpy(a.rows, rows, sizeof(int64_t) * (size_t)n_ranks);
-    a.weight = static_cast<const char *>(weight);
-    a.wdt = weight_dtype;
-    a.width = width;
-    a.eps = eps;
-    a.inv_width = 1.0f / (float)width;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const bool res = residual != nullptr;
     const bool nt = total * width * (esz * (1 + (res ? 1 : 0) + (sum_out ? 1 : 0)) + ysz) >= kStreamBytes;
-    if (dtype == DDP_F32) {
-        if (y_dtype == DDP_F32) return launch_norm<kF32, kF32>(a, res, nt, most, n_ranks, hs);
-        if (y_dtype == DDP_BF16) return launch_norm<kF32, kBF16>(a, res, nt, most, n_ranks, hs);
-        if (y_dtype == DDP_I8) return launch_norm<kF32, kI8>(a, res, nt, most, n_ranks, hs);
-        return launch_norm<kF32, kE4M3>(a, res, nt, most, n_ranks, hs);
-    }
-    if (y_dtype == DDP_BF16) return launch_norm<kBF16, kBF16>(a, res, nt, most, n_ranks, hs);
-    if (y_dtype == DDP_I8) return launch_norm<kBF16, kI8>(a, res, nt, most, n_ranks, hs);
-    return launch_norm<kBF16, kE4M3>(a, res, nt, most, n_ranks, hs);
+    return for_groups(n_ranks, [&](int32_t r0, int32_t nr) -> ddp_status_t {
+        NormArgs a;
+        std::memset(&a, 0, sizeof(a));
+        set_rows(&a.x, x, r0, nr, esz);
+        set_rows(&a.res, residual, r0, nr, esz);
+        set_rows(&a.sum, sum_out, r0, nr, esz);
+        set_rows(&a.y, y, r0, nr, ysz);
+        set_vecs(&a.scale, reinterpret_cast<const void *const *>(scale), r0, nr);
+        std::memcpy(a.rows, rows + r0, sizeof(int64_t) * (size_t)nr);
+        a.weight = static_cast<const char *>(weight);
+        a.wdt = weight_dtype;
+        a.width = width;
+        a.eps = eps;
+        a.inv_width = 1.0f / (float)width;
+        if (dtype == DDP_F32) {
+            if (y_dtype == DDP_F32) return launch_norm<kF32, kF32>(a, res, nt, most, nr, hs);
+            if (y_dtype == DDP_BF16) return launch_norm<kF32, kBF16>(a, res, nt, most, nr, hs);
+            if (y_dtype == DDP_I8) return launch_norm<kF32, kI8>(a, res, nt, most, nr, hs);
+            return launch_norm<kF32, kE4M3>(a, res, nt, most, nr, hs);
+        }
+        if (y_dtype == DDP_BF16) return launch_norm<kBF16, kBF16>(a, res, nt, most, nr, hs);
+        if (y_dtype == DDP_I8) return launch_norm<kBF16, kI8>(a, res, nt, most, nr, hs);
+        return launch_norm<kBF16, kE4M3>(a, res, nt, most, nr, hs);
+    });
 }
 
 int64_t ddp_rms_norm_grad_workspace(const int64_t *rows, int32_t n_ranks, int64_t width)
@@ -698,48 +700,56 @@ ddp_status_t ddp_rms_norm_grad(const int64_t *rows, int32_t n_ranks, int64_t wid
     }
     if ((st = check_operands(op, n, n_ranks)) != DDP_OK) return st;
     hipStream_t hs = static_cast<hipStream_t>(stream);
-    NormGradArgs a;
-    std::memset(&a, 0, sizeof(a));
-    set_rows(&a.s, total > 0 ? s : nullptr, n_ranks, esz);
-    set_rows(&a.dy, total > 0 ? dy : nullptr, n_ranks, ysz);
-    set_rows(&a.dsum, total > 0 ? dsum : nullptr, n_ranks, esz);
-    set_rows(&a.dx, total > 0 ? dx : nullptr, n_ranks, esz);
-    std::memcpy(a.rows, rows, sizeof(int64_t) * (size_t)n_ranks);
-    a.weight = static_cast<const char *>(weight);
-    a.wdt = weight_dtype;
-    a.part = dweight ? static_cast<float *>(workspace) : nullptr;
-    a.width = width;
-    a.part_width = padded(width);
-    a.eps = eps;
-    a.inv_width = 1.0f / (float)width;
+    const int64_t part_width = padded(width);
     const bool nt = total * width * (esz * (2 + (dsum ? 1 : 0)) + ysz) >= kStreamBytes;
-    const dim3 g((unsigned)blocks, (unsigned)n_ranks);
-    if (dtype == DDP_BF16)
-        launch_grad<kBF16, kBF16>(a, nt, g, hs);
-    else if (dy_dtype == DDP_F32)
-        launch_grad<kF32, kF32>(a, nt, g, hs);
-    else
-        launch_grad<kF32, kBF16>(a, nt, g, hs);
-    if ((st = launched("norm gradient kernel launch")) != DDP_OK || !dweight) return st;
-    DwArgs w;
-    std::memset(&w, 0, sizeof(w));
-    set_vecs(&w.dw, dweight, n_ranks);
-    w.width = width;
-    w.part_width = a.part_width;
-    w.last = width;
-    if (grad_held_vectors(width, vec)) {
-        const int64_t vecs = (width + vec - 1) / vec;
-        w.last = (vecs - 1) * vec;
-        w.shift = vecs * vec - width;
-    }
-    w.parts = (int32_t)blocks;
-    w.part = a.part;
-    w.dt = dweight_dtype;
-    w.accumulate = accumulate != 0;
-    return launch_split((width + kWave - 1) / kWave, kDwWaves * kWave,
-                        "weight gradient kernel launch", [&](int64_t b0, unsigned nb) {
-                            norm_grad_weight<<<dim3(nb, (unsigned)n_ranks), kDwWaves * kWave, 0, hs>>>(w, b0);
-                        });
+    st = for_groups(total > 0 || dweight ? n_ranks : 0, [&](int32_t r0, int32_t nr) {
+        NormGradArgs a;
+        std::memset(&a, 0, sizeof(a));
+        if (total > 0) {
+            set_rows(&a.s, s, r0, nr, esz);
+            set_rows(&a.dy, dy, r0, nr, ysz);
+            set_rows(&a.dsum, dsum, r0, nr, esz);
+            set_rows(&a.dx, dx, r0, nr, esz);
+            a.weight = static_cast<const char *>(weight);
+        }
+        std::memcpy(a.rows, rows + r0, sizeof(int64_t) * (size_t)nr);
+        a.wdt = weight_dtype;
+        a.part = dweight ? static_cast<float *>(workspace) + r0 * blocks * part_width : nullptr;
+        a.width = width;
+        a.part_width = part_width;
+        a.eps = eps;
+        a.inv_width = 1.0f / (float)width;
+        const dim3 g((unsigned)blocks, (unsigned)nr);
+        if (dtype == DDP_BF16)
+            launch_grad<kBF16, kBF16>(a, nt, g, hs);
+        else if (dy_dtype == DDP_F32)
+            launch_grad<kF32, kF32>(a, nt, g, hs);
+        else
+            launch_grad<kF32, kBF16>(a, nt, g, hs);
+        return launched("norm gradient kernel launch");
+    });
+    if (st != DDP_OK || !dweight) return st;
+    return for_groups(n_ranks, [&](int32_t r0, int32_t nr) {
+        DwArgs w;
+        std::memset(&w, 0, sizeof(w));
+        set_vecs(&w.dw, dweight, r0, nr);
+        w.width = width;
+        w.part_width = part_width;
+        w.last = width;
+        if (grad_held_vectors(width, vec)) {
+            const int64_t vecs = (width + vec - 1) / vec;
+            w.last = (vecs - 1) * vec;
+            w.shift = vecs * vec - width;
+        }
+        w.parts = (int32_t)blocks;
+        w.part = static_cast<const float *>(workspace) + r0 * blocks * part_width;
+        w.dt = dweight_dtype;
+        w.accumulate = accumulate != 0;
+        return launch_split((width + kWave - 1) / kWave, kDwWaves * kWave, "weight gradient kernel launch",
+                            [&](int64_t b0, unsigned nb) {
+            norm_grad_weight<<<dim3(nb, (unsigned)nr), kDwWaves * kWave, 0, hs>>>(w, b0);
+        });
+    });
 }
 
 }  // extern "C"

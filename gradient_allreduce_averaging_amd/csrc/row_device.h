@@ -9,26 +9,43 @@
 
 namespace ddp_detail {
 
-// One matrix operand of every rank; null addresses where it is absent.
+// Ranks of one launch; a call over more ranks is several launches.  A launch copies
+// its arguments into a buffer that the GPU reads: 64 ranks' addresses (3 to 4 KB)
+// cost 1 to 1.5 us a launch over 8 ranks', which a call on few tokens would feel.
+constexpr int kGroup = 8;
+
+// One matrix operand of the launch's ranks; null addresses where it is absent.
 struct RowPtrs {
-    char *p[DDP_MAX_RANKS];
+    char *p[kGroup];
     int64_t pitch;   // bytes from row to row
 };
 
 struct VecPtrs {
-    char *p[DDP_MAX_RANKS];
+    char *p[kGroup];
 };
 
-inline void set_rows(RowPtrs *d, const ddp_rows_t *m, int32_t n, int esz)
+// Ranks [r0, r0 + n) of a call's operands.
+inline void set_rows(RowPtrs *d, const ddp_rows_t *m, int32_t r0, int32_t n, int esz)
 {
     d->pitch = m ? m->stride * esz : 0;
-    for (int r = 0; r < n; ++r) d->p[r] = m ? static_cast<char *>(m->rank[r]) : nullptr;
+    for (int r = 0; r < n; ++r) d->p[r] = m ? static_cast<char *>(m->rank[r0 + r]) : nullptr;
 }
 
-inline void set_vecs(VecPtrs *d, const void *const *v, int32_t n)
+inline void set_vecs(VecPtrs *d, const void *const *v, int32_t r0, int32_t n)
 {
     for (int r = 0; r < n; ++r)
-        d->p[r] = v ? static_cast<char *>(const_cast<void *>(v[r])) : nullptr;
+        d->p[r] = v ? static_cast<char *>(const_cast<void *>(v[r0 + r])) : nullptr;
+}
+
+// Calls f(r0, n) for each group of at most kGroup ranks, until one fails.
+template <class F>
+ddp_status_t for_groups(int32_t n_ranks, F &&f)
+{
+    for (int32_t r0 = 0; r0 < n_ranks; r0 += kGroup) {
+        const ddp_status_t st = f(r0, n_ranks - r0 < kGroup ? n_ranks - r0 : kGroup);
+        if (st != DDP_OK) return st;
+    }
+    return DDP_OK;
 }
 
 constexpr int kWave = 64;

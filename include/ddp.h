@@ -469,7 +469,7 @@ typedef struct {
  *                  meaning.  NULL for other y_dtype
  * Squares are summed in f32: a row whose sum of s^2 passes 3.4e38 comes out
  * as zeros (NaN where s is infinite).  A row with a NaN comes out as NaN.
- * One launch.  No work where no rank has a row.
+ * One launch for each 8 ranks.  No work where no rank has a row.
  * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW, ALIAS, HIP. */
 DDP_API ddp_status_t ddp_rms_norm(const int64_t *rows, int32_t n_ranks, int64_t width,
                                   const ddp_rows_t *x, const ddp_rows_t *residual,
@@ -501,7 +501,7 @@ DDP_API ddp_status_t ddp_rms_norm(const int64_t *rows, int32_t n_ranks, int64_t 
  *               looked at without dweight
  * Sums are taken in f32 in an order that depends on the shape alone: the same
  * inputs give the same bits.  A rank without rows has a dweight of zeros.
- * Two launches (one without dweight).
+ * Two launches (one without dweight) for each 8 ranks.
  * Errors: as ddp_rms_norm, plus CAPACITY. */
 DDP_API ddp_status_t ddp_rms_norm_grad(const int64_t *rows, int32_t n_ranks, int64_t width,
                                        const ddp_rows_t *s, ddp_dtype_t dtype, const void *weight,
@@ -542,7 +542,7 @@ DDP_API int64_t ddp_rms_norm_grad_workspace(const int64_t *rows, int32_t n_ranks
  *   loss          device, one float
  *   row_loss      host array [n_ranks] of device pointers to rows[r] floats, or
  *                 NULL
- *   workspace     ddp_distill_workspace(rows, n_ranks, vocab) bytes
+ *   workspace     ddp_distill_workspace(rows, n_ranks, vocab, top) bytes
  * Sums are taken in f32 in an order that depends on the shape alone.
  * Errors: INVALID_ARG, UNSUPPORTED (a top, rank count, temperature or vocabulary
  * (2^31 - 1) beyond the library's), OVERFLOW, ALIAS, CAPACITY, HIP. */
@@ -572,7 +572,7 @@ DDP_API ddp_status_t ddp_distill_grad(const int64_t *rows, int32_t n_ranks, int6
                                       float *const *row_loss, void *workspace,
                                       int64_t workspace_bytes, void *stream);
 /* Bytes of workspace of either call, or -1 for arguments they would refuse. */
-DDP_API int64_t ddp_distill_workspace(const int64_t *rows, int32_t n_ranks, int64_t vocab);
+DDP_API int64_t ddp_distill_workspace(const int64_t *rows, int32_t n_ranks, int64_t vocab, int32_t top);
 
 /* ------------------------------------------------------------ no allocation
  * For callers that cannot allocate device memory: code under HIP graph

@@ -85,7 +85,8 @@ def test_vocabularies(ddp, vocab, dtype):
             assert gaps_untouched(d), what
 
 
-@pytest.mark.parametrize("rows", [[1], [2], [5, 3], [31], [64, 1, 64], [300], [129] * 8])
+@pytest.mark.parametrize("rows", [[1], [2], [5, 3], [31], [64, 1, 64], [300], [129] * 8, [3, 0, 5] * 6, [20] * 19,
+                                  [1] * 64])
 @pytest.mark.parametrize("vocab", [1000, 32000, 50257])
 def test_token_counts_with_masks(ddp, rows, vocab):
     z, t, i = _case(len(rows), rows, vocab, 24, "bf16", short=True)
@@ -291,7 +292,7 @@ def test_captured_and_replayed(ddp):
         z, t, i = _case(0, rows, vocab, top, "bf16")
         n_loss, rl = torch.empty(1, device="cuda"), [torch.empty(n, device="cuda") for n in rows]
         dz = [torch.empty_like(x) for x in z]
-        ws = torch.empty(ddp.distill_workspace(rows, vocab), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(ddp.distill_workspace(rows, vocab, top), dtype=torch.uint8, device="cuda")
         sets.append((z, t, i, n_loss, rl, dz, ws))
 
     def step(k):

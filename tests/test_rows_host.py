@@ -178,7 +178,7 @@ def test_distill_refuses(g):
     assert f(tw=(0, 13 * MB)) == INVALID
     assert f(rl=(0, 13 * MB)) == INVALID
     assert f(ws=None) == INVALID and f(ws=12 * MB + 4) == INVALID
-    need = ddp.distill_workspace((4, 4), 1000)
+    need = ddp.distill_workspace((4, 4), 1000, 8)
     assert f(size=need - 1) == CAPACITY
     # overlaps
     assert f(loss=10 * MB) == ALIAS
@@ -205,9 +205,10 @@ def test_workspace_sizes():
     assert L.ddp_rms_norm_grad_workspace(_rows(1), 0, 8) == -1
     assert L.ddp_rms_norm_grad_workspace(_rows(1), 1, 0) == -1
     assert L.ddp_rms_norm_grad_workspace(_rows(0), 1, 8) > 0
-    assert L.ddp_distill_workspace(None, 1, 8) == -1
-    assert L.ddp_distill_workspace(_rows(0), 1, 8) > 0
+    assert L.ddp_distill_workspace(None, 1, 8, 1) == -1
+    assert L.ddp_distill_workspace(_rows(0), 1, 8, 1) > 0
+    assert L.ddp_distill_workspace(_rows(1), 1, 8, 0) == -1 and L.ddp_distill_workspace(_rows(1), 1, 8, 1025) == -1
     with pytest.raises(ddp.DDPError):
-        ddp.distill_workspace([-1], 8)
+        ddp.distill_workspace([-1], 8, 1)
     with pytest.raises(ddp.DDPError):
         ddp.rms_norm_grad_workspace([1], 0)

@@ -39,7 +39,7 @@ namespace {
 constexpr int kFarThreads = 1024;     // distill_far, and the last sum of the loss
 constexpr int kLossThreads = 512;     // distill_row
 constexpr int kPartThreads = 256;     // distill_part, distill_emit
-constexpr int kMostParts = 256;       // blocks of distill_teacher, all ranks together
+constexpr int kMostParts = 512;       // blocks of distill_teacher, all ranks together
 constexpr int kMostSplits = 64;       // blocks to a token
 constexpr float kLn2 = 0.69314718f;
 constexpr float kNoEntry = -1.0f;
@@ -263,29 +263,6 @@ __device__ __forceinline__ void join_centres(const float *ms, const float *ss, i
     join_by(ms, ss, waves, m, s, [](float d) { return __builtin_amdgcn_exp2f(d); });
 }
 
-// dz at the entries' places within [lo, hi): every thread its own entries.  An
-// entry of an index named several times has the sum of their p, in their
-// order, so all of them store the same value.
-template <int DT, class Exp>
-__device__ __forceinline__ void emit_entries(const DistillArgs &a, const Entries &en, char *dz, Exp &&exp_z,
-                                             float inv_s, float c, int64_t lo, int64_t hi)
-{
-    const int padded = en.padded;
-    typedef int i32x4 __attribute__((ext_vector_type(4)));
-    for (int k = threadIdx.x; k < a.top; k += blockDim.x) {
-        const int32_t j = en.at[k];
-        if (j < lo || j >= hi) continue;
-        float p = 0.0f;
-        for (int i = 0; i < padded; i += 4) {
-            const i32x4 at = *reinterpret_cast<const i32x4 *>(&en.at[i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (at[e] == j) p += en.prob[i + e];
-        }
-        store_elem<DT>(dz, j, c * (exp_z(en.z[k]) * inv_s - p));
-    }
-}
-
 // A token that is not live: its loss, and zeros for its gradient, by the
 // threads of its block (elements [lo, hi) of the row).
 template <int DT>
@@ -319,82 +296,98 @@ __device__ __forceinline__ void note_row(const DistillArgs &a, int r, int64_t ro
 // equal indices gets does not depend on which of them was suspected.
 constexpr int kTeacherWords = 3;   // LDS words to an entry: place, p, bits
 
+struct TokenEntries {
+    int32_t *at;
+    float *prob;      // each entry's own p
+    uint32_t *bits;
+};
+__device__ __forceinline__ TokenEntries token_entries(const DistillArgs &a, int32_t *words)
+{
+    const int padded = padded_top(a.top);
+    return {words, reinterpret_cast<float *>(words + padded), reinterpret_cast<uint32_t *>(words + 2 * padded)};
+}
+
+// One wave, one token.  Returns whether it is live; *entropy receives E.
+__device__ __forceinline__ bool teacher_token(const DistillArgs &a, int r, int64_t row, const TokenEntries &te,
+                                              float *entropy)
+{
+    const int l = threadIdx.x % kWave, padded = padded_top(a.top);
+    const char *index = a.index.p[r] + row * a.index.pitch;
+    const char *teacher = a.teacher.p[r] + row * a.teacher.pitch;
+    int32_t *at = te.at;
+    float *prob = te.prob;
+    float tm = -INFINITY;
+    for (int k = l; k < padded; k += kWave) {
+        float t = 0.0f;
+        const int32_t j = k < a.top ? entry_of(a, index, teacher, k, &t) : -1;
+        at[k] = j;
+        prob[k] = t;
+        te.bits[k] = 0;
+        if (j >= 0) tm = fmaxf(tm, t);
+    }
+    tm = wave_all<OpMax>(tm);
+    if (tm == -INFINITY) return false;
+    float mass = 0.0f;
+    for (int k = l; k < padded; k += kWave) {
+        const float e = at[k] >= 0 ? exp_of(a, prob[k] - tm) : 0.0f;
+        prob[k] = e;
+        mass += e;
+    }
+    const float inv = 1.0f / wave_all<OpSum>(mass);
+    float ent = 0.0f;
+    float *out = a.prob + (a.first[r] + row) * a.top;
+    for (int k = l; k < padded; k += kWave) {
+        const float p = prob[k] * inv;
+        prob[k] = p;
+        if (p > 0.0f || p != p) ent += p * logf(p);
+        if (k < a.top) out[k] = at[k] >= 0 ? p : kNoEntry;
+    }
+    *entropy = wave_all<OpSum>(ent);
+    for (int k0 = 0; k0 < a.top; k0 += kWave) {
+        const int32_t mine = k0 + l < a.top ? at[k0 + l] : -1;
+        bool suspect = false;
+        if (mine >= 0) {
+            const uint32_t h = (uint32_t)mine * 0x9E3779B1u;
+            const uint32_t bit = 1u << (h >> 27);
+            suspect = atomicOr(&te.bits[((h & 0x7ffffffu) * (uint64_t)(uint32_t)padded) >> 27], bit) & bit;
+        }
+        uint64_t todo = __ballot(suspect);
+        while (todo) {
+            const int32_t j = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
+            todo &= todo - 1;
+            float p = 0.0f;
+            int first = -1;
+            for (int i0 = 0; i0 < a.top; i0 += kWave) {
+                const bool same = i0 + l < a.top && at[i0 + l] == j;
+                if (same) p += prob[i0 + l];
+                const uint64_t any = __ballot(same);
+                if (any && first < 0) first = i0 + __builtin_ctzll(any);
+            }
+            p = wave_all<OpSum>(p);
+            for (int i = l; i < a.top; i += kWave)
+                if (at[i] == j) out[i] = i == first ? p : kNoEntry;
+        }
+    }
+    return true;
+}
+
 __global__ void __launch_bounds__(kMostWaves * kWave) distill_teacher(DistillArgs a)
 {
     extern __shared__ __align__(16) int32_t entry_words[];
     __shared__ float lds[kMostWaves];
     const int r = blockIdx.y, l = threadIdx.x % kWave, wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
-    const int padded = padded_top(a.top);
-    int32_t *at = entry_words + wave * padded * kTeacherWords;
-    float *prob = reinterpret_cast<float *>(at + padded);
-    uint32_t *bits = reinterpret_cast<uint32_t *>(at + 2 * padded);
-    const int64_t step = (int64_t)gridDim.x * waves;
+    const TokenEntries te = token_entries(a, entry_words + wave * padded_top(a.top) * kTeacherWords);
     float d = 0.0f;
-    for (int64_t row = (int64_t)blockIdx.x * waves + wave; row < a.rows[r]; row += step) {
+    for (int64_t row = (int64_t)blockIdx.x * waves + wave; row < a.rows[r]; row += (int64_t)gridDim.x * waves) {
         const int64_t token = a.first[r] + row;
-        const char *index = a.index.p[r] + row * a.index.pitch;
-        const char *teacher = a.teacher.p[r] + row * a.teacher.pitch;
-        float tm = -INFINITY;
-        for (int k = l; k < padded; k += kWave) {
-            float t = 0.0f;
-            const int32_t j = k < a.top ? entry_of(a, index, teacher, k, &t) : -1;
-            at[k] = j;
-            prob[k] = t;
-            bits[k] = 0;
-            if (j >= 0) tm = fmaxf(tm, t);
-        }
         const float w = weight_of(a, r, row);
-        tm = wave_all<OpMax>(tm);
-        if (w == 0.0f || tm == -INFINITY) {
-            if (l == 0) a.w[token] = 0.0f;
-            continue;
-        }
-        d += w;
-        float mass = 0.0f;
-        for (int k = l; k < padded; k += kWave) {
-            const float e = at[k] >= 0 ? exp_of(a, prob[k] - tm) : 0.0f;
-            prob[k] = e;
-            mass += e;
-        }
-        const float inv = 1.0f / wave_all<OpSum>(mass);
         float ent = 0.0f;
-        float *out = a.prob + token * a.top;
-        for (int k = l; k < padded; k += kWave) {
-            const float p = prob[k] * inv;
-            prob[k] = p;
-            if (p > 0.0f || p != p) ent += p * logf(p);
-            if (k < a.top) out[k] = at[k] >= 0 ? p : kNoEntry;
-        }
-        ent = wave_all<OpSum>(ent);
+        const bool live = w > 0.0f && teacher_token(a, r, row, te, &ent);
         if (l == 0) {
-            a.w[token] = w;
+            a.w[token] = live ? w : 0.0f;
             a.loss_of[token] = ent;
         }
-        for (int k0 = 0; k0 < a.top; k0 += kWave) {
-            const int32_t mine = k0 + l < a.top ? at[k0 + l] : -1;
-            bool suspect = false;
-            if (mine >= 0) {
-                const uint32_t h = (uint32_t)mine * 0x9E3779B1u;
-                const uint32_t bit = 1u << (h >> 27);
-                suspect = atomicOr(&bits[((h & 0x7ffffffu) * (uint64_t)(uint32_t)padded) >> 27], bit) & bit;
-            }
-            uint64_t todo = __ballot(suspect);
-            while (todo) {
-                const int32_t j = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
-                todo &= todo - 1;
-                float p = 0.0f;
-                int first = -1;
-                for (int i0 = 0; i0 < a.top; i0 += kWave) {
-                    const bool same = i0 + l < a.top && at[i0 + l] == j;
-                    if (same) p += prob[i0 + l];
-                    const uint64_t any = __ballot(same);
-                    if (any && first < 0) first = i0 + __builtin_ctzll(any);
-                }
-                p = wave_all<OpSum>(p);
-                for (int i = l; i < a.top; i += kWave)
-                    if (at[i] == j) out[i] = i == first ? p : kNoEntry;
-            }
-        }
+        if (live) d += w;
     }
     d = l == 0 ? d : 0.0f;
     d = block_all<OpSum>(d, lds, waves);
@@ -415,11 +408,14 @@ struct Marks {
             p = a.prob[token * a.top + (int)threadIdx.x];
         }
     }
+    // The places within [from, to) count.
     template <int DT>
-    __device__ __forceinline__ void gather(const DistillArgs &a, const char *row_z, const Entries &en)
+    __device__ __forceinline__ void gather(const DistillArgs &a, const char *row_z, const Entries &en,
+                                           int64_t from, int64_t to)
     {
         if ((int)threadIdx.x < a.top) {
-            const uint32_t j = p == kNoEntry ? 0u : at;
+            if (at < from || at >= to) p = kNoEntry;
+            const uint32_t j = p == kNoEntry ? (uint32_t)from : at;
             z = DT == kF32 ? ld_elem<uint32_t>(row_z, j) : (uint32_t)ld_elem<uint16_t>(row_z, j);
             en.at[threadIdx.x] = (int32_t)at;
             en.prob[threadIdx.x] = p;
@@ -427,16 +423,18 @@ struct Marks {
     }
     template <int DT>
     __device__ __forceinline__ void stash(const DistillArgs &a, int r, int64_t row, int64_t token,
-                                          const char *row_z, const Entries &en) const
+                                          const char *row_z, const Entries &en, int64_t from,
+                                          int64_t to) const
     {
         if ((int)threadIdx.x < a.top) en.z[threadIdx.x] = __uint_as_float(DT == kF32 ? z : z << 16);
 #pragma unroll 1
         for (int k = threadIdx.x + blockDim.x; k < a.top; k += blockDim.x) {
             const uint32_t j = ld_elem<uint32_t>(a.index.p[r] + row * a.index.pitch + k * a.index_bytes, 0);
-            const float q = a.prob[token * a.top + k];
+            float q = a.prob[token * a.top + k];
+            if (j < from || j >= to) q = kNoEntry;
             en.at[k] = (int32_t)j;
             en.prob[k] = q;
-            en.z[k] = load_elem<DT>(row_z, q == kNoEntry ? 0 : (int64_t)j);
+            en.z[k] = load_elem<DT>(row_z, q == kNoEntry ? from : (int64_t)j);
         }
     }
 };
@@ -479,17 +477,23 @@ __device__ __forceinline__ void put_dot(const DistillArgs &a, Exchange &x, const
     t = wave_all<OpSum>(t);
     if (threadIdx.x % kWave == 0) x.dot[threadIdx.x / kWave] = t;
 }
-// Past the barrier that ends the stores: the entries' places again, and the row's
-// loss.  unit: of the dot, in natural logarithms.
+// Past the barrier that ends the stores: the entries' places again.
 template <int DT, class Exp>
-__device__ __forceinline__ void emit_marks(const DistillArgs &a, int r, int64_t row, float w, const Exchange &x,
-                                           const Entries &en, char *dz, Exp &&exp_z, float s, float c, float unit)
+__device__ __forceinline__ void emit_places(const DistillArgs &a, const Entries &en, char *dz, Exp &&exp_z, float s,
+                                            float c)
 {
     for (int k = threadIdx.x; k < a.top; k += blockDim.x) {
         const float p = en.prob[k];
         if (p == kNoEntry) continue;
         store_elem<DT>(dz, en.at[k], c * (exp_z(en.z[k]) * (1.0f / s) - p));
     }
+}
+// The same, and the row's loss.  unit: of the dot, in natural logarithms.
+template <int DT, class Exp>
+__device__ __forceinline__ void emit_marks(const DistillArgs &a, int r, int64_t row, float w, const Exchange &x,
+                                           const Entries &en, char *dz, Exp &&exp_z, float s, float c, float unit)
+{
+    emit_places<DT>(a, en, dz, exp_z, s, c);
     if (threadIdx.x < kWave) {
         const float dot = join_waves<OpSum>(x.dot, blockDim.x / kWave, 0.0f);
         if (threadIdx.x == 0) {
@@ -554,16 +558,6 @@ __device__ __forceinline__ float exp_at(const DistillArgs &a, float z, float c)
 // nothing but the type's lowest value, say) or are not finite.  Such rows go
 // through exp((z - m) / tau) with the subtraction first.
 __device__ __forceinline__ bool sane(float s) { return s >= FLT_MIN && s <= FLT_MAX; }
-
-// Elements by which bf16 rows start past a 4-byte boundary.  16-byte accesses
-// off one take 35 % longer (4 x 512 x 50257: 61 us, x 50264: 45), so the vectors
-// of a row start on one: the first element of an odd row is taken by itself,
-// with the last few that fill no vector.
-template <int DT>
-__device__ __forceinline__ int odd_start(const char *row)
-{
-    return DT == kBF16 ? (int)(reinterpret_cast<uintptr_t>(row) >> 1 & 1) : 0;
-}
 
 // The pair of this thread's share of the n logits at z, the block's threads
 // taking U vectors each to a step: (m, s), or with FAST (c, s) of exp_at.
@@ -725,8 +719,8 @@ __device__ __forceinline__ bool grad_of_row(const DistillArgs &a, int r, int64_t
     mk.load(a, r, row, token);
     float m, s;
     stats_of<DT, FAST, false>(a, z, a.vocab, &m, &s);
-    mk.gather<DT>(a, z, en);
-    mk.stash<DT>(a, r, row, token, z, en);
+    mk.gather<DT>(a, z, en, 0, a.vocab);
+    mk.stash<DT>(a, r, row, token, z, en, 0, a.vocab);
     put_den(a, x);
     wave_join<FAST>(a, &m, &s);
     put_pair(x, m, s);
@@ -811,7 +805,7 @@ __global__ void __launch_bounds__(kMostWaves * kWave) distill_held(DistillArgs a
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         v[i] = ld_vec<true, u32x4>(z + (uint32_t)inside(place(i * threads + (int)threadIdx.x)) * size);
-    mk.gather<DT>(a, z, en);
+    mk.gather<DT>(a, z, en, 0, n);
     const int wave0 = __builtin_amdgcn_readfirstlane((int)threadIdx.x & ~(kWave - 1));
     float own = -FLT_MAX, s = 0.0f, c_own = 0.0f;
 #pragma unroll
@@ -847,7 +841,7 @@ __global__ void __launch_bounds__(kMostWaves * kWave) distill_held(DistillArgs a
             }
         }
     }
-    mk.stash<DT>(a, r, row, token, z, en);
+    mk.stash<DT>(a, r, row, token, z, en, 0, n);
     put_den(a, x);
     float c_row = c_own, s_row = s;
     wave_join<true>(a, &c_row, &s_row);
@@ -886,43 +880,65 @@ __global__ void __launch_bounds__(kMostWaves * kWave) distill_held(DistillArgs a
 
 // ---------------------------------------------------------------- several blocks to a token
 
-// First pass: (m, s) of a split; split 0 also looks up the teacher and notes the
-// row's weight and its loss but for m and s.
-template <int DT>
+// First pass: (m, s) of a split; one block more for each token looks up the
+// teacher and notes the row's weight and its loss but for m and s.  GRAD: and
+// leaves the entries as distill_teacher does.
+template <int DT, bool GRAD>
 __global__ void __launch_bounds__(kPartThreads) distill_part(DistillArgs a)
 {
-    const Entries en = entries_of(a);
+    extern __shared__ __align__(16) int32_t entry_words[];
     __shared__ float ms[kMostWaves], ss[kMostWaves];
-    const int r = blockIdx.z, split = blockIdx.x;
+    const int r = blockIdx.z, split = blockIdx.x, l = threadIdx.x % kWave;
     const int64_t row = blockIdx.y;
     if (row >= a.rows[r]) return;
     const int64_t token = a.first[r] + row;
     const float w = weight_of(a, r, row);
-    if (w == 0.0f) {
-        if (split == 0 && threadIdx.x == 0) note_row(a, r, row, 0.0f, 0.0f);
-        return;
-    }
     const char *z = a.z.p[r] + row * a.z.pitch;
-    const int64_t lo = split * a.seg, hi = split + 1 == a.splits ? a.vocab : lo + a.seg;
-    float m, s;
-    FirstEntry first;
-    const bool look = split == 0 && threadIdx.x < kWave;
-    if (look) first.load(a, r, row);
-    stats_of<DT, false, false>(a, z + lo * kSize<DT>, hi - lo, &m, &s);
-    wave_join<false>(a, &m, &s);
-    if (threadIdx.x % kWave == 0) {
-        ms[threadIdx.x / kWave] = m;
-        ss[threadIdx.x / kWave] = s;
-    }
-    if (look) {
-        first.gather<DT>(a, z, 0, a.vocab);
-        const bool live = teacher_of<DT>(a, r, row, en, first, z, 0, a.vocab);
+    if (split == a.splits) {
+        if (threadIdx.x >= kWave) return;
+        bool live = false;
         float ref = 0.0f, base = 0.0f;
-        if (live) base = divergence_of(a, en, &ref);
-        if (threadIdx.x == 0) {
+        if (GRAD) {
+            const TokenEntries te = token_entries(a, entry_words);
+            live = w > 0.0f && teacher_token(a, r, row, te, &base);
+            if (live) {
+                // the logits at the entries, in place of the bits
+                float *zs = reinterpret_cast<float *>(te.bits);
+                ref = -FLT_MAX;
+                for (int k = l; k < a.top; k += kWave) {
+                    zs[k] = te.at[k] >= 0 ? load_elem<DT>(z, te.at[k]) : 0.0f;
+                    if (te.prob[k] > 0.0f) ref = fmaxf(ref, zs[k]);
+                }
+                ref = wave_all<OpMax>(ref);
+                float dot = 0.0f;
+                for (int k = l; k < a.top; k += kWave) {
+                    const float p = te.prob[k];
+                    if (p > 0.0f || p != p) dot += p * (zs[k] - ref);
+                }
+                base -= wave_all<OpSum>(dot) * a.inv_tau;
+            }
+        } else if (w > 0.0f) {
+            const Entries en = entries_of(a);
+            FirstEntry first;
+            first.load(a, r, row);
+            first.gather<DT>(a, z, 0, a.vocab);
+            live = teacher_of<DT>(a, r, row, en, first, z, 0, a.vocab);
+            if (live) base = divergence_of(a, en, &ref);
+        }
+        if (l == 0) {
             note_row(a, r, row, live ? w : 0.0f, live ? base : 0.0f);
             a.ref[token] = ref;
         }
+        return;
+    }
+    if (w == 0.0f) return;
+    const int64_t lo = split * a.seg, hi = split + 1 == a.splits ? a.vocab : lo + a.seg;
+    float m, s;
+    stats_of<DT, false, false>(a, z + lo * kSize<DT>, hi - lo, &m, &s);
+    wave_join<false>(a, &m, &s);
+    if (l == 0) {
+        ms[threadIdx.x / kWave] = m;
+        ss[threadIdx.x / kWave] = s;
     }
     __syncthreads();
     join_pairs(a, ms, ss, kPartThreads / kWave, &m, &s);
@@ -955,8 +971,8 @@ __global__ void __launch_bounds__(kPartThreads) distill_emit(DistillArgs a)
         return;
     }
     const char *z = a.z.p[r] + row * a.z.pitch;
-    FirstEntry first;
-    if (threadIdx.x < kWave) first.load(a, r, row);
+    Marks mk;
+    mk.load(a, r, row, token);
     // every wave joins the row's parts for itself
     const int l = threadIdx.x % kWave;
     float m = -FLT_MAX, s = 0.0f;
@@ -964,20 +980,18 @@ __global__ void __launch_bounds__(kPartThreads) distill_emit(DistillArgs a)
         m = a.part[(token * a.splits + l) * 2];
         s = a.part[(token * a.splits + l) * 2 + 1];
     }
-    wave_join<false>(a, &m, &s);
     float d = 0.0f;
     for (int64_t i = threadIdx.x; i < a.tokens; i += kPartThreads) d += a.w[i];
+    mk.gather<DT>(a, z, en, lo, hi);
+    wave_join<false>(a, &m, &s);
     d = block_all<OpSum>(d, lds, kPartThreads / kWave);
-    if (threadIdx.x < kWave) {
-        first.gather<DT>(a, z, lo, hi);
-        teacher_of<DT>(a, r, row, en, first, z, lo, hi);
-    }
+    mk.stash<DT>(a, r, row, token, z, en, lo, hi);
     __syncthreads();   // the logits at the entries are read before any is written
-    const float c = a.scale * (w / d), inv_s = 1.0f / s;
+    const float c = a.scale * (w / d);
     auto exp_z = [&](float q) { return exp_of(a, q - m); };
-    emit_of<DT>(z + lo * kSize<DT>, dz + lo * kSize<DT>, hi - lo, inv_s * c, exp_z);
+    emit_of<DT>(z + lo * kSize<DT>, dz + lo * kSize<DT>, hi - lo, c / s, exp_z);
     __syncthreads();
-    emit_entries<DT>(a, en, dz, exp_z, inv_s, c, lo, hi);
+    emit_places<DT>(a, en, dz, exp_z, s, c);
 }
 
 // ---------------------------------------------------------------- host
@@ -1000,7 +1014,7 @@ Splits splits_of(int64_t tokens, int64_t vocab)
 int64_t distill_bytes(int64_t tokens, int64_t vocab, int64_t top)
 {
     const int64_t n = splits_of(tokens, vocab).n;
-    const int64_t floats = kMostParts + 3 * tokens + (n ? 2 * n : top) * tokens;
+    const int64_t floats = kMostParts + (3 + 2 * n + top) * tokens;
     return (floats * 4 + 15) / 16 * 16;
 }
 
@@ -1017,7 +1031,7 @@ constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 // Threads of a block that steps through a row of `vecs` vectors, at most `most`.
 int far_threads(int64_t vecs, int most)
 {
-    return (int)std::min<int64_t>(most, (vecs + kWave - 1) / kWave * kWave);
+    return (int)std::max<int64_t>(kWave, std::min<int64_t>(most, (vecs + kWave - 1) / kWave * kWave));
 }
 
 template <int DT, bool NT>
@@ -1046,7 +1060,9 @@ ddp_status_t launch_grad(const DistillArgs &a, int64_t most, hipStream_t st)
 template <int DT>
 ddp_status_t launch_loss(const DistillArgs &a, int64_t most, hipStream_t st)
 {
-    const int threads = far_threads((a.vocab + kVec<DT> - 1) / kVec<DT>, kLossThreads);
+    // four vectors to a thread, one step of stats_of, where that is fewer threads than most:
+    // 8 x 2048 x 2000 bf16 43 us with 256 threads
+    const int threads = far_threads((a.vocab / kVec<DT> + 3) / 4, kLossThreads);
     return launch_split(most, threads, "distillation kernel launch", [&](int64_t b0, unsigned nb) {
         distill_row<DT><<<dim3(nb, (unsigned)a.n_ranks), threads, entry_bytes(a.top), st>>>(a, b0);
     });
@@ -1117,7 +1133,8 @@ ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_
     all.w = all.den + kMostParts;
     all.loss_of = all.w + total;
     all.ref = all.loss_of + total;
-    all.part = all.prob = all.ref + total;
+    all.part = all.ref + total;
+    all.prob = all.part + 2 * sp.n * total;
     all.loss = loss;
     // distill_teacher: a wave to a token where there are that many, within 64 KB of LDS to a block
     const int64_t per_wave = 4 * kTeacherWords * (int64_t)padded_top(top);
@@ -1144,11 +1161,16 @@ ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_
     hipStream_t hs = static_cast<hipStream_t>(stream);
     if (sp.n) {   // several blocks to a token
         st = for_groups(n_ranks, [&](int32_t r0, int32_t nr) {
-            const dim3 g((unsigned)sp.n, (unsigned)most, (unsigned)nr);
-            if (dtype == DDP_F32)
-                distill_part<kF32><<<g, kPartThreads, entry_bytes(top), hs>>>(group(r0, nr));
-            else
-                distill_part<kBF16><<<g, kPartThreads, entry_bytes(top), hs>>>(group(r0, nr));
+            const dim3 g((unsigned)sp.n + 1, (unsigned)most, (unsigned)nr);
+            const unsigned lds = entry_bytes(top);
+            const DistillArgs a = group(r0, nr);
+            if (dtype == DDP_F32) {
+                if (grad) distill_part<kF32, true><<<g, kPartThreads, lds, hs>>>(a);
+                else distill_part<kF32, false><<<g, kPartThreads, lds, hs>>>(a);
+            } else {
+                if (grad) distill_part<kBF16, true><<<g, kPartThreads, lds, hs>>>(a);
+                else distill_part<kBF16, false><<<g, kPartThreads, lds, hs>>>(a);
+            }
             return launched("distillation kernel launch");
         });
         if (st != DDP_OK) return st;

@@ -201,12 +201,13 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_held(NormArgs a, int6
     if (row >= a.rows[r]) return;
     const char *x = a.x.p[r] + row * a.x.pitch;
     const char *res = RES ? a.res.p[r] + row * a.res.pitch : nullptr;
+    const int shift = odd_start<DT>(x) ? V - 1 : 0;
     Piece pc[NV];
     u32x4 s[NV], q[NV];
     Weight<V> wt[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        pc[i] = piece_of<V>(i * threads + (int)threadIdx.x, (int)a.width);
+        pc[i] = piece_of<V>(i * threads + (int)threadIdx.x, (int)a.width, shift);
         s[i] = ld_vec<NT, u32x4>(x + pc[i].at * size);
         if (RES) q[i] = ld_vec<NT, u32x4>(res + pc[i].at * size);
     }
@@ -227,12 +228,12 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_held(NormArgs a, int6
         float t = 0.0f;
 #pragma unroll
         for (int e = 0; e < V; ++e) t = __builtin_fmaf(value<V, DT>(s[i], e), value<V, DT>(s[i], e), t);
-        if (pc[i].skip) {
+        if (pc[i].off) {
             t = 0.0f;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float v = value<V, DT>(s[i], e);
-                t = e >= (int)pc[i].skip ? __builtin_fmaf(v, v, t) : t;
+                t = counts<V>(pc[i], e) ? __builtin_fmaf(v, v, t) : t;
             }
         }
         ss += t;
@@ -286,7 +287,8 @@ struct NormGradArgs {
     int64_t rows[kGroup];
     const char *weight;
     float *part;        // [n_ranks][blocks][part_width] partial weight gradients, or null
-    int64_t width, part_width;   // part_width: width up to a multiple of 8
+    int64_t width, part_width;   // part_width: room for the width in vectors
+    int odd_stride;     // bf16 rows an odd number of elements apart
     int wdt;
     float eps, inv_width;
 };
@@ -349,11 +351,19 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArg
     u32x4 s[NV], q[NV];
     Dy d[NV];
     Weight<V> wt[NV];
-    // this block's rows: a stretch of its rank's
-    const int64_t per = (rows + gridDim.x - 1) / gridDim.x;
-    const int64_t end = min(rows, (blockIdx.x + 1) * per);
-    int64_t row = blockIdx.x * per;
-    auto fetch = [&](int64_t at_row) {
+    // This block's rows: a stretch of its rank's.  Where rows alternate between
+    // starting on and off a 4-byte boundary (a.odd_stride), even blocks take
+    // the even rows and odd blocks the odd ones, so that a block's vectors have one
+    // place (and its weight gradient one order).
+    const int kind = a.odd_stride ? (int)blockIdx.x & 1 : 0, step = a.odd_stride ? 2 : 1;
+    const int64_t mine = (rows - kind + step - 1) / step;                         // rows of the kind
+    const int64_t blocks = a.odd_stride ? ((int64_t)gridDim.x + 1 - kind) / 2 : gridDim.x;   // blocks
+    const int64_t per = (mine + blocks - 1) / blocks, nth = blockIdx.x / step;
+    const int64_t end = min(mine, (nth + 1) * per);
+    int64_t at_row = nth * per;
+    const int shift = odd_start<DT>(a.s.p[r] + kind * a.s.pitch) ? V - 1 : 0;
+    auto fetch = [&](int64_t k) {
+        const int64_t at_row = k * step + kind;
         const char *sp = a.s.p[r] + at_row * a.s.pitch, *dp = a.dy.p[r] + at_row * a.dy.pitch;
         const char *qp = a.dsum.p[r] + at_row * a.dsum.pitch;
 #pragma unroll
@@ -365,19 +375,20 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArg
     };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        pc[i] = piece_of<V>(i * threads + (int)threadIdx.x, (int)a.width);
+        pc[i] = piece_of<V>(i * threads + (int)threadIdx.x, (int)a.width, shift);
         wt[i].load(a.weight, a.wdt, pc[i].at);
         q[i] = u32x4{0, 0, 0, 0};
     }
-    if (PF && row < end) fetch(row);
+    if (PF && at_row < end) fetch(at_row);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         wt[i].values(a.weight, a.wdt, w[i]);
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[i][e] = 0.0f;
     }
-    for (; row < end; ++row) {
-        if (!PF) fetch(row);
+    for (; at_row < end; ++at_row) {
+        const int64_t row = at_row * step + kind;
+        if (!PF) fetch(at_row);
         u32x4 s0[NV], q0[NV];
         Dy d0[NV];
         float ss = 0.0f, gs = 0.0f;
@@ -393,20 +404,20 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArg
                 t = __builtin_fmaf(v, v, t);
                 u = __builtin_fmaf(value<V, YT>(d0[i], e) * w[i][e], v, u);
             }
-            if (pc[i].skip) {
+            if (pc[i].off) {
                 t = u = 0.0f;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float v = value<V, DT>(s0[i], e);
-                    const bool mine = e >= (int)pc[i].skip;
-                    t = mine ? __builtin_fmaf(v, v, t) : t;
-                    u = mine ? __builtin_fmaf(value<V, YT>(d0[i], e) * w[i][e], v, u) : u;
+                    const bool ours = counts<V>(pc[i], e);
+                    t = ours ? __builtin_fmaf(v, v, t) : t;
+                    u = ours ? __builtin_fmaf(value<V, YT>(d0[i], e) * w[i][e], v, u) : u;
                 }
             }
             ss += t;
             gs += u;
         }
-        if (PF && row + 1 < end) fetch(row + 1);
+        if (PF && at_row + 1 < end) fetch(at_row + 1);
         ss = wave_all<OpSum>(ss);
         gs = wave_all<OpSum>(gs);
         if (waves > 1) {
@@ -448,27 +459,41 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArg
 // each of its waves a stretch of the blocks, joined in the waves' order.
 struct DwArgs {
     VecPtrs dw;
+    RowPtrs s;              // where odd blocks' rows start (norm_grad_held)
     int64_t width, part_width;
-    int64_t last, shift;    // columns from `last` on lie `shift` further (a row's last vector)
     int32_t parts;
+    int vec, odd_stride;    // vec: of norm_grad_held's vectors, 0 for norm_grad_rows
     const float *part;
     int dt, accumulate;
 };
 
 constexpr int kDwWaves = 8;
 
+// Column j's place in a block's partial sums: in its vector (Piece).
+__device__ __forceinline__ int64_t part_place(int64_t j, int64_t width, int vec, int shift)
+{
+    if (!vec) return j;
+    const int64_t k = (j + shift) / vec, at = max((int64_t)0, min(k * vec - shift, width - vec));
+    return k * vec + j - at;
+}
+
 __global__ void __launch_bounds__(kDwWaves * kWave) norm_grad_weight(DwArgs a, int64_t first_block)
 {
     __shared__ float lds[kDwWaves][kWave];
     const int r = blockIdx.y, wave = threadIdx.x / kWave, l = threadIdx.x % kWave;
-    const int64_t j = (first_block + blockIdx.x) * kWave + l;
-    const float *p = a.part + (int64_t)r * a.parts * a.part_width +
-                     (j < a.last ? j : j < a.width ? j + a.shift : 0);
+    const int64_t j = (first_block + blockIdx.x) * kWave + l, col = min(j, a.width - 1);
+    const float *p = a.part + (int64_t)r * a.parts * a.part_width;
+    int64_t place[2];   // in an even block's sums and in an odd one's
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+        const bool odd = a.vec == 8 && a.s.p[r] && odd_start<kBF16>(a.s.p[r] + (a.odd_stride ? kind : 0) * a.s.pitch);
+        place[kind] = part_place(col, a.width, a.vec, odd ? a.vec - 1 : 0);
+    }
     const int per = (a.parts + kDwWaves - 1) / kDwWaves;
     const int b0 = wave * per, b1 = min(b0 + per, a.parts);
     float t = 0.0f;
 #pragma unroll 8
-    for (int b = b0; b < b1; ++b) t += p[b * a.part_width];
+    for (int b = b0; b < b1; ++b) t += p[b * a.part_width + ((b & 1) ? place[1] : place[0])];
     lds[wave][l] = t;
     __syncthreads();
     if (wave || j >= a.width) return;
@@ -480,15 +505,21 @@ __global__ void __launch_bounds__(kDwWaves * kWave) norm_grad_weight(DwArgs a, i
         store_elem<kBF16>(dw, j, a.accumulate ? load_elem<kBF16>(dw, j) + t : t);
 }
 
-int64_t padded(int64_t width) { return (width + 7) / 8 * 8; }
+// Elements a row may need beyond its width for its vectors to start on a 4-byte
+// boundary (Piece), and the room for its partial weight gradient either way.
+int row_shift(int dtype, const ddp_rows_t *m, const int64_t *rows, int32_t n)
+{
+    return dtype == DDP_BF16 && odd_rows(m, rows, n) ? kVec<kBF16> - 1 : 0;
+}
+int64_t padded(int64_t width) { return (width + kVec<kBF16> - 1 + 7) / 8 * 8; }
 
 int dtype_bytes(int dt) { return dt == DDP_F32 ? 4 : dt == DDP_BF16 ? 2 : 1; }
 bool eight(int dt) { return dt == DDP_I8 || dt == DDP_E4M3; }
 
 bool eps_ok(float eps) { return eps >= 0.0f && std::isfinite(eps); }
 
-// The kernel for rows of `width` elements, `vec` to a 16-byte vector: the
-// vectors each thread of a block holds, as few as let a block of at most 16
+// The kernel for rows of `width` elements (and their shift), `vec` to a 16-byte
+// vector: the vectors each thread of a block holds, as few as let a block of at most 16
 // waves hold the row (more, smaller shares per thread measured as fast or
 // faster: 8 x 2048 x 4096 bf16 forward 87.0 us with 1, 87.2 us with 2), or 0
 // where no block can and the row is read from memory in every pass.
@@ -496,7 +527,7 @@ constexpr int64_t kMostThreads = kMostWaves * kWave;
 int held_vectors(int64_t width, int64_t vec, int most)
 {
     const int64_t vecs = (width + vec - 1) / vec;
-    if (width < vec || vecs > most * kMostThreads) return 0;
+    if (width < 2 * vec || vecs > most * kMostThreads) return 0;
     return vecs <= kMostThreads ? 1 : vecs <= 2 * kMostThreads ? 2 : 4;
 }
 int held_threads(int64_t width, int64_t vec, int nv)
@@ -527,16 +558,16 @@ int64_t grad_blocks(int64_t most, int32_t n_ranks, int64_t width, int64_t vec)
 }
 
 template <int DT, int YT, bool RES, bool NT>
-ddp_status_t launch_norm_as(const NormArgs &a, int64_t most, int32_t n_ranks, hipStream_t st)
+ddp_status_t launch_norm_as(const NormArgs &a, int shift, int64_t most, int32_t n_ranks, hipStream_t st)
 {
     constexpr int V = kVec<DT>;
-    const int nv = held_vectors(a.width, V, 4);
+    const int nv = held_vectors(a.width + shift, V, 4);
     if (!nv) {
         const dim3 g((unsigned)std::min(most, kMostGridRows), (unsigned)n_ranks);
         norm_rows<DT, YT, RES><<<g, kNormThreads, 0, st>>>(a);
         return launched("norm kernel launch");
     }
-    const int threads = held_threads(a.width, V, nv);
+    const int threads = held_threads(a.width + shift, V, nv);
     return launch_split(most, threads, "norm kernel launch", [&](int64_t b0, unsigned nb) {
         const dim3 g(nb, (unsigned)n_ranks);
         if (nv == 1)
@@ -549,11 +580,11 @@ ddp_status_t launch_norm_as(const NormArgs &a, int64_t most, int32_t n_ranks, hi
 }
 
 template <int DT, int YT, bool NT>
-void launch_grad_as(const NormGradArgs &a, dim3 g, hipStream_t st)
+void launch_grad_as(const NormGradArgs &a, int shift, dim3 g, hipStream_t st)
 {
     constexpr int V = kVec<DT>;
-    const int nv = grad_held_vectors(a.width, V);
-    const int threads = nv ? held_threads(a.width, V, nv) : kNormThreads;
+    const int nv = grad_held_vectors(a.width + shift, V);
+    const int threads = nv ? held_threads(a.width + shift, V, nv) : kNormThreads;
     if (nv == 1)
         norm_grad_held<DT, YT, 1, true, NT><<<g, threads, 0, st>>>(a);
     else if (nv == 2)
@@ -572,20 +603,20 @@ void launch_grad_as(const NormGradArgs &a, dim3 g, hipStream_t st)
 constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 
 template <int DT, int YT>
-ddp_status_t launch_norm(const NormArgs &a, bool res, bool nt, int64_t most, int32_t n, hipStream_t st)
+ddp_status_t launch_norm(const NormArgs &a, int shift, bool res, bool nt, int64_t most, int32_t n, hipStream_t st)
 {
     if (res)
-        return nt ? launch_norm_as<DT, YT, true, true>(a, most, n, st)
-                  : launch_norm_as<DT, YT, true, false>(a, most, n, st);
-    return nt ? launch_norm_as<DT, YT, false, true>(a, most, n, st)
-              : launch_norm_as<DT, YT, false, false>(a, most, n, st);
+        return nt ? launch_norm_as<DT, YT, true, true>(a, shift, most, n, st)
+                  : launch_norm_as<DT, YT, true, false>(a, shift, most, n, st);
+    return nt ? launch_norm_as<DT, YT, false, true>(a, shift, most, n, st)
+              : launch_norm_as<DT, YT, false, false>(a, shift, most, n, st);
 }
 
 template <int DT, int YT>
-void launch_grad(const NormGradArgs &a, bool nt, dim3 g, hipStream_t st)
+void launch_grad(const NormGradArgs &a, int shift, bool nt, dim3 g, hipStream_t st)
 {
-    if (nt) launch_grad_as<DT, YT, true>(a, g, st);
-    else launch_grad_as<DT, YT, false>(a, g, st);
+    if (nt) launch_grad_as<DT, YT, true>(a, shift, g, st);
+    else launch_grad_as<DT, YT, false>(a, shift, g, st);
 }
 
 
@@ -623,6 +654,7 @@ ddp_status_t ddp_rms_norm(const int64_t *rows, int32_t n_ranks, int64_t width, c
     if ((st = check_operands(op, n, n_ranks)) != DDP_OK) return st;
     hipStream_t hs = static_cast<hipStream_t>(stream);
     const bool res = residual != nullptr;
+    const int shift = row_shift(dtype, x, rows, n_ranks);
     const bool nt = total * width * (esz * (1 + (res ? 1 : 0) + (sum_out ? 1 : 0)) + ysz) >= kStreamBytes;
     return for_groups(n_ranks, [&](int32_t r0, int32_t nr) -> ddp_status_t {
         NormArgs a;
@@ -639,14 +671,14 @@ ddp_status_t ddp_rms_norm(const int64_t *rows, int32_t n_ranks, int64_t width, c
         a.eps = eps;
         a.inv_width = 1.0f / (float)width;
         if (dtype == DDP_F32) {
-            if (y_dtype == DDP_F32) return launch_norm<kF32, kF32>(a, res, nt, most, nr, hs);
-            if (y_dtype == DDP_BF16) return launch_norm<kF32, kBF16>(a, res, nt, most, nr, hs);
-            if (y_dtype == DDP_I8) return launch_norm<kF32, kI8>(a, res, nt, most, nr, hs);
-            return launch_norm<kF32, kE4M3>(a, res, nt, most, nr, hs);
+            if (y_dtype == DDP_F32) return launch_norm<kF32, kF32>(a, shift, res, nt, most, nr, hs);
+            if (y_dtype == DDP_BF16) return launch_norm<kF32, kBF16>(a, shift, res, nt, most, nr, hs);
+            if (y_dtype == DDP_I8) return launch_norm<kF32, kI8>(a, shift, res, nt, most, nr, hs);
+            return launch_norm<kF32, kE4M3>(a, shift, res, nt, most, nr, hs);
         }
-        if (y_dtype == DDP_BF16) return launch_norm<kBF16, kBF16>(a, res, nt, most, nr, hs);
-        if (y_dtype == DDP_I8) return launch_norm<kBF16, kI8>(a, res, nt, most, nr, hs);
-        return launch_norm<kBF16, kE4M3>(a, res, nt, most, nr, hs);
+        if (y_dtype == DDP_BF16) return launch_norm<kBF16, kBF16>(a, shift, res, nt, most, nr, hs);
+        if (y_dtype == DDP_I8) return launch_norm<kBF16, kI8>(a, shift, res, nt, most, nr, hs);
+        return launch_norm<kBF16, kE4M3>(a, shift, res, nt, most, nr, hs);
     });
 }
 
@@ -654,8 +686,9 @@ int64_t ddp_rms_norm_grad_workspace(const int64_t *rows, int32_t n_ranks, int64_
 {
     int64_t total, most;
     if (check_shape(rows, n_ranks, width, &total, &most) != DDP_OK) return -1;
-    // either dtype's number of blocks
-    const int64_t blocks = std::max(grad_blocks(most, n_ranks, width, 4), grad_blocks(most, n_ranks, width, 8));
+    // the number of blocks of either dtype, of rows on and off a 4-byte boundary
+    const int64_t blocks = std::max({grad_blocks(most, n_ranks, width, 4), grad_blocks(most, n_ranks, width, 8),
+                                     grad_blocks(most, n_ranks, width + 7, 8)});
     return (int64_t)sizeof(float) * n_ranks * blocks * padded(width);
 }
 
@@ -679,7 +712,9 @@ ddp_status_t ddp_rms_norm_grad(const int64_t *rows, int32_t n_ranks, int64_t wid
         return DDP_ERR_INVALID_ARG;
     const int esz = dtype_size(dtype), ysz = dtype_size(dy_dtype);
     const int64_t vec = vec_elems(dtype);
-    const int64_t blocks = grad_blocks(most, n_ranks, width, vec);
+    const int shift = total > 0 ? row_shift(dtype, s, rows, n_ranks) : 0;
+    const int odd_stride = shift && most > 1 && s->stride % 2;
+    const int64_t blocks = grad_blocks(most, n_ranks, width + shift, vec);
     const int64_t need = ddp_rms_norm_grad_workspace(rows, n_ranks, width);
     if (dweight) {
         if (!workspace || !aligned(workspace, 16)) return DDP_ERR_INVALID_ARG;
@@ -717,15 +752,16 @@ ddp_status_t ddp_rms_norm_grad(const int64_t *rows, int32_t n_ranks, int64_t wid
         a.part = dweight ? static_cast<float *>(workspace) + r0 * blocks * part_width : nullptr;
         a.width = width;
         a.part_width = part_width;
+        a.odd_stride = odd_stride;
         a.eps = eps;
         a.inv_width = 1.0f / (float)width;
         const dim3 g((unsigned)blocks, (unsigned)nr);
         if (dtype == DDP_BF16)
-            launch_grad<kBF16, kBF16>(a, nt, g, hs);
+            launch_grad<kBF16, kBF16>(a, shift, nt, g, hs);
         else if (dy_dtype == DDP_F32)
-            launch_grad<kF32, kF32>(a, nt, g, hs);
+            launch_grad<kF32, kF32>(a, shift, nt, g, hs);
         else
-            launch_grad<kF32, kBF16>(a, nt, g, hs);
+            launch_grad<kF32, kBF16>(a, shift, nt, g, hs);
         return launched("norm gradient kernel launch");
     });
     if (st != DDP_OK || !dweight) return st;
@@ -735,12 +771,9 @@ ddp_status_t ddp_rms_norm_grad(const int64_t *rows, int32_t n_ranks, int64_t wid
         set_vecs(&w.dw, dweight, r0, nr);
         w.width = width;
         w.part_width = part_width;
-        w.last = width;
-        if (grad_held_vectors(width, vec)) {
-            const int64_t vecs = (width + vec - 1) / vec;
-            w.last = (vecs - 1) * vec;
-            w.shift = vecs * vec - width;
-        }
+        if (total > 0) set_rows(&w.s, s, r0, nr, esz);
+        w.vec = grad_held_vectors(width + shift, vec) ? (int)vec : 0;
+        w.odd_stride = odd_stride;
         w.parts = (int32_t)blocks;
         w.part = static_cast<const float *>(workspace) + r0 * blocks * part_width;
         w.dt = dweight_dtype;

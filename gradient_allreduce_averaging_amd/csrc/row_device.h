@@ -174,24 +174,44 @@ __device__ __forceinline__ void st_vec(char *p, const V &v)
         *reinterpret_cast<VU *>(p) = v;
 }
 
-// A row of n >= V elements as vectors of V: vector k covers [k * V, k * V + V),
-// but for the last one, which ends with the row and so may share elements with
-// the one before.  Both hold (and store) the same values there; sums count an
-// element once, for the vector that starts at or before k * V.  So no row end
-// takes a path by element.
+// bf16 rows may start off a 4-byte boundary, and 16-byte accesses off one take a
+// third longer (the norm of 8 x 2048 x 4095 bf16: 111 us so, 4096: 90).  So the
+// vectors of a row start on one: by one element (7 of 8 before the row).
+template <int DT>
+__device__ __forceinline__ int odd_start(const char *row)
+{
+    return DT == kBF16 ? (int)(reinterpret_cast<uintptr_t>(row) >> 1 & 1) : 0;
+}
+// Whether a matrix of bf16 has such rows, on the host.
+inline bool odd_rows(const ddp_rows_t *m, const int64_t *rows, int32_t n)
+{
+    for (int r = 0; r < n; ++r)
+        if (rows[r] > 0 && ((reinterpret_cast<uintptr_t>(m->rank[r]) & 2) || (rows[r] > 1 && m->stride % 2)))
+            return true;
+    return false;
+}
+
+// A row of n >= V elements as vectors of V: vector k's place is elements
+// [k * V - shift, + V), shift 0 or V - 1 (odd_start), but for the first and the
+// last it may reach out of the row: they are moved inside, and share elements
+// with their neighbours.  Both hold (and store) the same values there; sums
+// count an element for the vector whose place it is.  So no row end takes a path
+// by element.
 struct Piece {
-    uint32_t at;      // first element
-    uint32_t skip;    // elements of it that another vector counts: 0 but for the last vector,
-                      // V or more past the end
+    int at;     // first element
+    int off;    // its place less `at`: not 0 where it was moved, V or more past the row
 };
 template <int V>
-__device__ __forceinline__ Piece piece_of(int k, int n)
+__device__ __forceinline__ Piece piece_of(int k, int n, int shift)
 {
-    const int j = k * V, at = min(j, n - V);
-    return {(uint32_t)at, (uint32_t)(j - at)};
+    const int j = k * V - shift, at = max(0, min(j, n - V));
+    return {at, j - at};
 }
 template <int V>
-__device__ __forceinline__ bool owned(const Piece &p) { return p.skip < V; }
+__device__ __forceinline__ bool owned(const Piece &p) { return p.off < V; }
+// Whether element e of a moved vector counts for it.
+template <int V>
+__device__ __forceinline__ bool counts(const Piece &p, int e) { return (uint32_t)(e - p.off) < (uint32_t)V; }
 
 template <int DT> constexpr int kSize = DT == kF32 ? 4 : 2;
 

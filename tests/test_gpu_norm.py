@@ -123,6 +123,31 @@ def test_many_ranks_and_rows(ddp, n_ranks):
         check_norm_grad(dx[r], dw[r], x[r], w, d[r], None, EPS, what=r)
 
 
+@pytest.mark.parametrize("width", [9, 15, 513, 4095, 4097, 8191, 16377, 16384])
+@pytest.mark.parametrize("first", [0, 1])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_bf16_rows_on_and_off_a_word(ddp, width, first, pad):
+    """Rows that start on a 4-byte boundary, off one, or in turn, in ranks of 1 to many rows: every
+    element of the sums, and the weight gradient of both kinds of rows together."""
+    rows = [1, 2, 0, 600]
+    x = [matrix(_rand(r, n, width, "bf16"), pad, first + r % 2) for r, n in enumerate(rows)]
+    d = [matrix(_rand(9 + r, n, width, "bf16"), pad, first) for r, n in enumerate(rows)]
+    w = _weight(1, width, "f32")
+    y = [_empty(n, width, "bf16", pad, 3) for n in rows]
+    dx = [_empty(n, width, "bf16", pad, first) for n in rows]
+    dw = [torch.full((width,), math.nan, device="cuda") for _ in rows]
+    ddp.rms_norm(x, w, y, eps=EPS)
+    ddp.rms_norm_grad(x, w, d, dx, dweight=dw, eps=EPS)
+    torch.cuda.synchronize()
+    for r, n in enumerate(rows):
+        if n:
+            check_norm(y[r], x[r], w, EPS, what=r)
+            check_norm_grad(dx[r], dw[r], x[r], w, d[r], None, EPS, what=r)
+            assert gaps_untouched(y[r]) and gaps_untouched(dx[r])
+        else:
+            assert (dw[r] == 0).all()
+
+
 def test_more_rows_than_a_grid(ddp):
     rows, width = 70001, 9
     x = _rand(0, rows, width, "f32").cuda()

@@ -15,12 +15,21 @@
 // exp((z - m) / tau) = exp((z - m_own) / tau) exp((m_own - m) / tau).  So each
 // logit has one exp and nothing waits for the row's largest before that.
 //
-// Three kernels, chosen by the vocabulary and the number of tokens:
-//   distill_held   a block to a token, the row's exponentials in registers;
-//   distill_far    a block to a token, the row read twice: vocabularies that
-//                  registers do not hold (or shorter than a vector);
+// The kernels of a call, by the vocabulary and the number of tokens:
+//   distill_row    the loss, a block to a token;
+//   distill_held   the gradient, a block to a token, the row in registers;
+//   distill_far    the same, the row read twice: vocabularies that registers do
+//                  not hold (or shorter than a vector);
+//   distill_teacher   ahead of these two, a wave to a token: the entries, D;
 //   distill_part,  few tokens: several blocks to a token, joined through the
-//   distill_emit   workspace, the second pass over rows the caches still hold.
+//   distill_emit   workspace, the second pass over rows the caches still hold;
+//   distill_one    a single token;
+//   distill_total  the loss of the call, where no other kernel has it.
+//
+// At 8 x 512 x 32000 bf16 the gradient moves 524 MB in 110 us: distill_held 98
+// (5.4 TB/s; 72 without its stores, no faster without its exps), distill_teacher 7,
+// distill_total 4.6.  The loss of 4 x 512 x 50257, a quarter masked, reads 154 MB
+// in 35 us, distill_row 32 (4.8 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -505,30 +514,52 @@ __device__ __forceinline__ void emit_marks(const DistillArgs &a, int r, int64_t 
 
 // ---------------------------------------------------------------- the loss
 
-// loss = sum of w row / sum of w, by one block.  With splits the rows' parts
-// are joined here first.
-__device__ void finish(const DistillArgs &a, float *lds)
+// The losses of split rows, which loss_of has but for m and s: 2^k lanes to a
+// token, each with the pair of one split, so that no load waits for another (the
+// loss of 1 x 131072 7.1 us, 15.4 with a thread to a token).
+// Adds weights and weighted losses to *d and *l.
+__device__ __forceinline__ void join_splits(const DistillArgs &a, float *d, float *l)
 {
-    const int waves = blockDim.x / kWave;
-    float d = 0.0f, l = 0.0f;
-    for (int64_t i = threadIdx.x; i < a.tokens; i += blockDim.x) {
-        const float w = a.w[i];
-        if (!(w > 0.0f)) continue;
-        float loss = a.loss_of[i];
-        if (a.splits) {
-            const float *part = a.part + i * a.splits * 2;
-            float m = -FLT_MAX, s = 0.0f;
-            for (int k = 0; k < a.splits; ++k) m = fmaxf(m, part[2 * k]);
-            for (int k = 0; k < a.splits; ++k) s += part[2 * k + 1] * exp_of(a, part[2 * k] - m);
-            loss = a.tau * a.tau * (loss + ((m - a.ref[i]) * a.inv_tau + logf(s)));
+    int lanes = 1;
+    while (lanes < a.splits) lanes *= 2;
+    const int k = (int)threadIdx.x % lanes, step = (int)blockDim.x / lanes;
+    for (int64_t i = (int)threadIdx.x / lanes; i < a.tokens; i += step) {
+        float own = -FLT_MAX, s = 0.0f;
+        if (k < a.splits) {
+            own = a.part[(i * a.splits + k) * 2];
+            s = a.part[(i * a.splits + k) * 2 + 1];
+        }
+        const float w = a.w[i], base = a.loss_of[i], ref = a.ref[i];
+        float m = own;
+        for (int o = lanes / 2; o; o /= 2) m = fmaxf(m, __shfl_xor(m, o));
+        s *= exp_of(a, own - m);
+        for (int o = lanes / 2; o; o /= 2) s += __shfl_xor(s, o);
+        if (k == 0 && w > 0.0f) {
+            const float loss = a.tau * a.tau * (base + ((m - ref) * a.inv_tau + logf(s)));
             // the losses of this launch's ranks (every launch adds up all tokens)
             for (int r = 0; r < a.n_ranks; ++r)
                 if (a.row_loss.p[r] && i >= a.first[r] && i < a.first[r] + a.rows[r])
                     st_elem<float>(a.row_loss.p[r], i - a.first[r], loss);
+            *d += w;
+            *l += w * loss;
         }
-        d += w;
-        l += w * loss;
     }
+}
+
+// loss = sum of w row / sum of w, by one block.
+__device__ __forceinline__ void finish(const DistillArgs &a, float *lds)
+{
+    const int waves = blockDim.x / kWave;
+    float d = 0.0f, l = 0.0f;
+    if (a.splits)
+        join_splits(a, &d, &l);
+    else
+        for (int64_t i = threadIdx.x; i < a.tokens; i += blockDim.x) {
+            const float w = a.w[i];
+            if (!(w > 0.0f)) continue;
+            d += w;
+            l += w * a.loss_of[i];
+        }
     d = block_all<OpSum>(d, lds, waves);
     l = block_all<OpSum>(l, lds, waves);
     if (threadIdx.x == 0) *a.loss = d > 0.0f ? l / d : 0.0f;
@@ -758,6 +789,48 @@ __global__ void __launch_bounds__(kFarThreads) distill_far(DistillArgs a, int64_
     if (grad_of_row<DT, true>(a, r, row, w, z, dz, en, x)) return;
     __syncthreads();
     grad_of_row<DT, false>(a, r, row, w, z, dz, en, x);
+}
+
+// A call on one token, by one block and in one launch: the teacher's entries
+// (GRAD: into the workspace, as distill_teacher leaves them), the row, and the
+// loss.
+template <int DT, bool GRAD>
+__global__ void __launch_bounds__(kFarThreads) distill_one(DistillArgs a)
+{
+    extern __shared__ __align__(16) int32_t entry_words[];
+    __shared__ float pairs[2 * kMostWaves];
+    __shared__ Exchange x;
+    __shared__ int alive;
+    const int r = blockIdx.y;
+    if (a.rows[r] == 0) return;   // not the rank that has it
+    const float w = weight_of(a, r, 0);
+    const char *z = a.z.p[r];
+    const Entries en = entries_of(a);
+    if (GRAD) {
+        if (threadIdx.x < kWave) {
+            float ent = 0.0f;
+            const bool live = w > 0.0f && teacher_token(a, r, 0, token_entries(a, entry_words), &ent);
+            if (threadIdx.x == 0) {
+                a.den[0] = w;
+                a.loss_of[0] = ent;
+                alive = live;
+            }
+        }
+        __syncthreads();
+        if (!alive) {
+            if (threadIdx.x == 0) note_row(a, r, 0, 0.0f, 0.0f);
+            emit_zeros<DT>(a.dz.p[r], 0, a.vocab);
+        } else if (!grad_of_row<DT, true>(a, r, 0, w, z, a.dz.p[r], en, x)) {
+            __syncthreads();
+            grad_of_row<DT, false>(a, r, 0, w, z, a.dz.p[r], en, x);
+        }
+    } else if (w == 0.0f) {
+        if (threadIdx.x == 0) note_row(a, r, 0, 0.0f, 0.0f);
+    } else if (!loss_of_row<DT, true>(a, r, 0, w, z, en, pairs)) {
+        __syncthreads();
+        loss_of_row<DT, false>(a, r, 0, w, z, en, pairs);
+    }
+    if (threadIdx.x == 0) *a.loss = a.w[0] > 0.0f ? a.loss_of[0] : 0.0f;   // as this thread noted them
 }
 
 // What follows takes the vectors' elements apart anew: kept apart from one use
@@ -996,6 +1069,12 @@ __global__ void __launch_bounds__(kPartThreads) distill_emit(DistillArgs a)
 
 // ---------------------------------------------------------------- host
 
+// The largest vocabularies of which a single token is one block's work, in one
+// launch.  bf16, against several blocks and two launches (three below 4096): the
+// loss of 32000 logits 4.5 us and 6.7, of 65536 5.6 and 6.9, of 131072 8.1 and
+// 7.1; the gradient of 4000 6.5 and 9.9, of 8192 6.7 and 7.6, of 32000 9.1 and 7.8.
+constexpr int64_t kOneLoss = 65536, kOneGrad = 8192;
+
 // Blocks to a token: enough to give the 256 CUs two blocks each, of at least
 // 2048 logits; 0 where one block to a token does.
 struct Splits {
@@ -1061,7 +1140,7 @@ template <int DT>
 ddp_status_t launch_loss(const DistillArgs &a, int64_t most, hipStream_t st)
 {
     // four vectors to a thread, one step of stats_of, where that is fewer threads than most:
-    // 8 x 2048 x 2000 bf16 43 us with 256 threads
+    // 8 x 2048 x 2000 bf16 20 us with 64 threads, 43 with 256
     const int threads = far_threads((a.vocab / kVec<DT> + 3) / 4, kLossThreads);
     return launch_split(most, threads, "distillation kernel launch", [&](int64_t b0, unsigned nb) {
         distill_row<DT><<<dim3(nb, (unsigned)a.n_ranks), threads, entry_bytes(a.top), st>>>(a, b0);
@@ -1159,6 +1238,23 @@ ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_
         return a;
     };
     hipStream_t hs = static_cast<hipStream_t>(stream);
+    if (total == 1 && vocab <= (grad ? kOneGrad : kOneLoss)) {
+        all.parts = 1;
+        return for_groups(n_ranks, [&](int32_t r0, int32_t nr) {
+            const DistillArgs a = group(r0, nr);
+            const int threads = far_threads((vocab / vec_elems(dtype) + 3) / 4, kFarThreads);
+            const dim3 g(1, (unsigned)nr);
+            const unsigned lds = entry_bytes(top);
+            if (dtype == DDP_F32) {
+                if (grad) distill_one<kF32, true><<<g, threads, lds, hs>>>(a);
+                else distill_one<kF32, false><<<g, threads, lds, hs>>>(a);
+            } else {
+                if (grad) distill_one<kBF16, true><<<g, threads, lds, hs>>>(a);
+                else distill_one<kBF16, false><<<g, threads, lds, hs>>>(a);
+            }
+            return launched("distillation kernel launch");
+        });
+    }
     if (sp.n) {   // several blocks to a token
         st = for_groups(n_ranks, [&](int32_t r0, int32_t nr) {
             const dim3 g((unsigned)sp.n + 1, (unsigned)most, (unsigned)nr);

@@ -219,6 +219,31 @@ def test_in_place(ddp, dtype, rows, vocab):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("vocab", [1, 9, 1000, 32003, 131072, 131073])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("top", [1, 5, 700])
+def test_one_token(ddp, vocab, dtype, top):
+    """One token in the whole call, on the first rank, the last or one past the first launch's:
+    alone, with indices named twice, in place, masked."""
+    for rows in ([1], [0, 0, 1], [0] * 9 + [1, 0]):
+        at = rows.index(1)
+        z, t, i = _case(vocab + at, rows, vocab, top, dtype, idt=torch.int32 if at else torch.int64, pad=at, shift=at)
+        for x in i:
+            x[:, -1] = x[:, 0]
+        _run(ddp, z, t, i, tau=1.2, grad=False, what=rows)
+        _, rl, dz = _run(ddp, z, t, i, [torch.full((n,), 0.3, device="cuda") for n in rows], tau=1.2, what=rows)
+        loss, rl2, _ = _run(ddp, z, t, i, tau=1.2, dz=z, check=False)
+        assert torch.equal(dz[at], z[at]) and torch.equal(rl[at], rl2[at]) and torch.equal(loss, rl2[at])
+        z[at][0] = math.nan
+        for w, n in ((0.0, None), (1.0, -1)):
+            if n is not None:
+                i[at][0] = n
+            weight = [torch.full((k,), w, device="cuda") for k in rows]
+            for grad in (False, True):
+                loss, rl, dz = _run(ddp, z, t, i, weight, grad=grad, check=False)
+                assert loss == 0 and rl[at][0] == 0 and (dz is None or (dz[at] == 0).all())
+
+
 def test_average_over_ranks_is_the_gradient_of_the_whole(ddp):
     """Ranks with unequal numbers of live tokens: the 1/N average of what follows from dlogits
     is the gradient of the mean over all tokens, in 64 bits by autograd."""

@@ -1216,9 +1216,10 @@ ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_
     all.part = all.ref + total;
     all.prob = all.part + 2 * sp.n * total;
     all.loss = loss;
-    // distill_teacher: a wave to a token where there are that many, within 64 KB of LDS to a block
+    // distill_teacher: a wave to a token where there are that many, within 64 KB of LDS to a
+    // block, its waves' sums among them
     const int64_t per_wave = 4 * kTeacherWords * (int64_t)padded_top(top);
-    const int64_t waves = std::min<int64_t>(kMostWaves, 65536 / per_wave);
+    const int64_t waves = std::min<int64_t>(kMostWaves, (65536 - 4 * kMostWaves) / per_wave);
     const int64_t blocks =
         std::max<int64_t>(1, std::min<int64_t>((most + waves - 1) / waves, kMostParts / n_ranks));
     all.parts = (int32_t)(blocks * n_ranks);
@@ -1310,7 +1311,9 @@ extern "C" {
 int64_t ddp_distill_workspace(const int64_t *rows, int32_t n_ranks, int64_t vocab, int32_t top)
 {
     int64_t total, most;
-    if (check_shape(rows, n_ranks, vocab, &total, &most) != DDP_OK || top < 1 || top > DDP_MAX_TOP) return -1;
+    if (check_shape(rows, n_ranks, vocab, &total, &most) != DDP_OK || vocab > INT32_MAX || top < 1 ||
+        top > DDP_MAX_TOP)
+        return -1;
     return distill_bytes(total, vocab, top);
 }
 

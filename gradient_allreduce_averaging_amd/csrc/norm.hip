@@ -48,6 +48,14 @@ struct NormArgs {
     float eps, inv_width;
 };
 
+// 1 / sqrt(v) by the hardware's instruction (1 ulp), which takes v below the least normal
+// float for zero: such a v goes through an exact power of two.
+__device__ __forceinline__ float inv_root(float v)
+{
+    const bool low = v < 0x1p-100f;
+    return __builtin_amdgcn_rsqf(low ? v * 0x1p64f : v) * (low ? 0x1p32f : 1.0f);
+}
+
 // s of element j: the residual added in f32 and rounded to the dtype.
 template <int DT, bool RES>
 __device__ __forceinline__ float sum_elem(const char *x, const char *res, int64_t j)
@@ -246,7 +254,7 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_held(NormArgs a, int6
         for (int i = 0; i < NV; ++i)
             if (owned<V>(pc[i])) st_vec<NT>(sum + pc[i].at * size, s[i]);
     }
-    const float rho = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, a.inv_width, a.eps));
+    const float rho = inv_root(__builtin_fmaf(ss, a.inv_width, a.eps));
     float y[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -318,14 +326,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_rows(NormGradArgs a)
         ss = block_all<OpSum>(ss, lds, waves);
         gs = block_all<OpSum>(gs, lds, waves);
         const float rho = 1.0f / sqrtf(ss / (float)W + a.eps);
-        const float c = rho * rho * (gs / (float)W);
+        const float c = rho * (gs / (float)W);
         for (int64_t j = threadIdx.x; j < W; j += kNormThreads) {
             const float v = load_elem<DT>(s, j), d = load_elem<YT>(dy, j);
             const float g = d * (a.weight ? load_as(a.weight, j, a.wdt) : 1.0f);
-            float o = rho * (g - v * c);
+            float o = rho * (g - v * rho * c);
             if (ds) o = load_elem<DT>(ds, j) + o;
             store_elem<DT>(dx, j, o);
-            if (part) part[j] += d * v * rho;
+            if (part) part[j] += d * (v * rho);
         }
     }
 }
@@ -431,8 +439,8 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArg
             ss = join_waves<OpSum>(slot, waves, 0.0f);
             gs = join_waves<OpSum>(slot + kMostWaves, waves, 0.0f);
         }
-        const float rho = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, a.inv_width, a.eps));
-        const float c = rho * rho * (gs * a.inv_width);
+        const float rho = inv_root(__builtin_fmaf(ss, a.inv_width, a.eps));
+        const float c = rho * (gs * a.inv_width);
         char *dx = a.dx.p[r] + row * a.dx.pitch;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -440,9 +448,10 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArg
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float v = value<V, DT>(s0[i], e), g = value<V, YT>(d0[i], e);
-                o[e] = rho * (g * w[i][e] - v * c);
+                const float h = v * rho;   // taken first: rho^2 of a row of tiny values overflows
+                o[e] = rho * (g * w[i][e] - h * c);
                 if (has_q) o[e] = value<V, DT>(q0[i], e) + o[e];
-                acc[i][e] = __builtin_fmaf(g, v * rho, acc[i][e]);
+                acc[i][e] = __builtin_fmaf(g, h, acc[i][e]);
             }
             if (owned<V>(pc[i])) st_values<V, DT, NT>(dx + pc[i].at * size, o);
         }
@@ -618,7 +627,6 @@ void launch_grad(const NormGradArgs &a, int shift, bool nt, dim3 g, hipStream_t 
     if (nt) launch_grad_as<DT, YT, true>(a, shift, g, st);
     else launch_grad_as<DT, YT, false>(a, shift, g, st);
 }
-
 
 }  // namespace
 

@@ -142,7 +142,6 @@ __device__ __forceinline__ float load_as(const char *p, int64_t i, int dt)
     return dt == kF32 ? ld_elem<float>(p, i) : widen_bf16(ld_elem<uint16_t>(p, i));
 }
 
-
 // ---------------------------------------------------------------- vectors
 // A lane's piece of a row: 16 bytes of f32 or bf16, at any element alignment.
 template <int DT> constexpr int kVec = DT == kF32 ? 4 : 8;

@@ -468,7 +468,9 @@ typedef struct {
  *                  codes 0; a row with a NaN has a NaN scale and codes of no
  *                  meaning.  NULL for other y_dtype
  * Squares are summed in f32: a row whose sum of s^2 passes 3.4e38 comes out
- * as zeros (NaN where s is infinite).  A row with a NaN comes out as NaN.
+ * as zeros (NaN where s is infinite).  A row with a NaN comes out as NaN.  With
+ * eps = 0 a row of values about 1e-19 and below loses accuracy, as their squares
+ * do, and a row of zeros is NaN.
  * One launch for each 8 ranks.  No work where no rank has a row.
  * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW, ALIAS, HIP. */
 DDP_API ddp_status_t ddp_rms_norm(const int64_t *rows, int32_t n_ranks, int64_t width,
@@ -499,8 +501,8 @@ DDP_API ddp_status_t ddp_rms_norm(const int64_t *rows, int32_t n_ranks, int64_t 
  *               ddp_accumulate)
  *   workspace   ddp_rms_norm_grad_workspace(rows, n_ranks, width) bytes; not
  *               looked at without dweight
- * Sums are taken in f32 in an order that depends on the shape alone: the same
- * inputs give the same bits.  A rank without rows has a dweight of zeros.
+ * Sums are taken in f32 in an order that depends on the shape and the rows'
+ * alignment alone: the same inputs give the same bits.  A rank without rows has a dweight of zeros.
  * Two launches (one without dweight) for each 8 ranks.
  * Errors: as ddp_rms_norm, plus CAPACITY. */
 DDP_API ddp_status_t ddp_rms_norm_grad(const int64_t *rows, int32_t n_ranks, int64_t width,
@@ -543,7 +545,8 @@ DDP_API int64_t ddp_rms_norm_grad_workspace(const int64_t *rows, int32_t n_ranks
  *   row_loss      host array [n_ranks] of device pointers to rows[r] floats, or
  *                 NULL
  *   workspace     ddp_distill_workspace(rows, n_ranks, vocab, top) bytes
- * Sums are taken in f32 in an order that depends on the shape alone.
+ * Sums are taken in f32 in an order that depends on the shape and the rows'
+ * alignment alone: the same inputs give the same bits.
  * Errors: INVALID_ARG, UNSUPPORTED (a top, rank count, temperature or vocabulary
  * (2^31 - 1) beyond the library's), OVERFLOW, ALIAS, CAPACITY, HIP. */
 DDP_API ddp_status_t ddp_distill_loss(const int64_t *rows, int32_t n_ranks, int64_t vocab,

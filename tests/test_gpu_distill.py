@@ -159,6 +159,13 @@ def test_an_index_named_twice(ddp, vocab, top, many):
     _run(ddp, z, t, i, tau=1.3, grad=False)
 
 
+@pytest.mark.parametrize("top", [2, 63, 64, 65, 340, 364, 420, 780, 1023])
+def test_numbers_of_entries(ddp, top):
+    z, t, i = _case(top, [270], 2003, top, "bf16", tdt="bf16", pad=1)
+    _run(ddp, z, t, i, tau=1.7, what=top)
+    _run(ddp, z, t, i, tau=1.7, grad=False, what=top)
+
+
 @pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("vocab", [5, 33, 4096, 50257, 70000])

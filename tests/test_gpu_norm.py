@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from gpu_util import torch_cuda
-from rows_util import check_norm, check_norm_grad, gaps_untouched, matrix, norm_sum
+from rows_util import U, chain, check_norm, check_norm_grad, gaps_untouched, matrix, norm_64, norm_grad_64, norm_rel, norm_sum
 
 pytestmark = pytest.mark.gpu
 
@@ -222,6 +222,35 @@ def test_unusual_values(ddp, width, out):
         else:
             assert torch.isnan(sc[4]) and torch.isnan(sc[5]) and sc[1] == 0
             assert (y[1].float() == 0).all()
+
+
+@pytest.mark.parametrize("width", [7, 48, 4096, 40009])
+def test_tiny_rows_without_eps(ddp, width):
+    """Rows whose mean square lies below the least normal float, forward and backward."""
+    s = _rand(0, 5, width, "f32").cuda() * 2.0 ** -64
+    dy, w = _rand(1, 5, width, "f32").cuda(), _weight(2, width, "f32")
+    w = w.cuda()
+    s[0] = 2.0 ** -66
+    s[1] *= 2.0 ** 30   # an ordinary one
+    y, dx, dw = torch.empty_like(s), torch.empty_like(s), torch.empty(width, device="cuda")
+    ddp.rms_norm([s], w, [y], eps=0.0)
+    ddp.rms_norm_grad([s], w, [dy], [dx], dweight=[dw], eps=0.0)
+    want, _ = norm_64(s, w, 0.0)
+    # a square, a partial sum and the mean are each off by at most half a step of 2^-149, so the mean
+    # of squares of 2^-134 or more by (chain + 2) 2^-150 / width, and 2^-150 for its own rounding; the
+    # root has half of that, beside the errors of ordinary rows
+    mean = s.double().square().mean(1, keepdim=True)
+    assert float(mean.min()) > 2.0 ** -134
+    low = ((width + 2 * chain(width)) / width + 1) * 2.0 ** -150 / mean
+    rel = norm_rel(width) + low
+    assert ((y.double() - want).abs() <= want.abs() * (rel + 2 * U)).all()
+    wdx, wdw = norm_grad_64(s, w, dy, None, 0.0)
+    h, g = s.double(), dy.double() * w.double()
+    rho = mean.rsqrt()
+    big = rho * (g.abs() + (h * rho).abs() * rho * (g * h).abs().mean(1, keepdim=True))
+    # the products g s are off by 2^-150 too, which rho ~ 2^64 leaves far below U
+    assert ((dx.double() - wdx).abs() <= big * (4 * rel + (chain(width) + 16) * U)).all()
+    assert ((dw.double() - wdw).abs() <= ((dy.double() * h * rho).abs() * (rel + 16 * U)).sum(0)).all()
 
 
 def test_weight_that_is_zero_or_not_finite(ddp):

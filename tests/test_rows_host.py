@@ -208,6 +208,7 @@ def test_workspace_sizes():
     assert L.ddp_distill_workspace(None, 1, 8, 1) == -1
     assert L.ddp_distill_workspace(_rows(0), 1, 8, 1) > 0
     assert L.ddp_distill_workspace(_rows(1), 1, 8, 0) == -1 and L.ddp_distill_workspace(_rows(1), 1, 8, 1025) == -1
+    assert L.ddp_distill_workspace(_rows(1), 1, 2 ** 31, 1) == -1
     with pytest.raises(ddp.DDPError):
         ddp.distill_workspace([-1], 8, 1)
     with pytest.raises(ddp.DDPError):

@@ -35,7 +35,7 @@ namespace {
 constexpr int kI8 = 2;
 constexpr int kE4M3 = 3;
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 256;   // norm_rows, norm_grad_rows, narrow rows of the backward
 constexpr int64_t kMostGridRows = 1 << 16;   // blocks to a rank of norm_rows, which step through its rows
 
 struct NormArgs {
@@ -45,6 +45,7 @@ struct NormArgs {
     const char *weight;
     int64_t width;
     int wdt;
+    int lanes;          // to a row, where rows are narrow; 0: a block to a row
     float eps, inv_width;
 };
 
@@ -193,20 +194,27 @@ __global__ void __launch_bounds__(kNormThreads) norm_rows(NormArgs a)
     }
 }
 
-// The row in registers: a block of up to 16 waves owns a row, each thread NV
+// The row in registers: a team of threads owns a row, each of them NV
 // 16-byte vectors of it (vector i of thread t is the row's vector
 // i * threads + t), so x (and the residual) are read once and every output is
-// written once.
-template <int DT, int YT, bool RES, int NV, bool NT>
-__global__ void __launch_bounds__(kMostWaves * kWave) norm_held(NormArgs a, int64_t first_row)
+// written once.  The team is a block of up to 16 waves, or, for narrow rows (NVS = 0:
+// one vector to a thread), a group of a.lanes lanes of a block's one wave.
+template <int DT, int YT, bool RES, int NVS, bool NT>
+__global__ void __launch_bounds__(NVS ? kMostWaves * kWave : kWave) norm_held(NormArgs a, int64_t first)
 {
-    constexpr int V = kVec<DT>, size = kSize<DT>;
+    constexpr int V = kVec<DT>, size = kSize<DT>, NV = NVS ? NVS : 1;
     constexpr bool k8 = YT == kI8 || YT == kE4M3;
     __shared__ float lds[2 * kMostWaves];
     int turn = 0;
-    const int r = blockIdx.y, threads = blockDim.x, waves = threads / kWave;
-    const int64_t row = first_row + blockIdx.x;
+    const int r = blockIdx.y, threads = NVS ? blockDim.x : a.lanes;
+    const int me = NVS ? (int)threadIdx.x : (int)threadIdx.x & (threads - 1);
+    int64_t row = first + blockIdx.x;
+    if (!NVS) row = row * (kWave / threads) + (int)threadIdx.x / threads;
     if (row >= a.rows[r]) return;
+    auto team = [&](auto op, float v) {
+        using Op = decltype(op);
+        return NVS ? team_all<Op>(v, lds, &turn, threads / kWave) : group_all<Op>(v, threads);
+    };
     const char *x = a.x.p[r] + row * a.x.pitch;
     const char *res = RES ? a.res.p[r] + row * a.res.pitch : nullptr;
     const int shift = odd_start<DT>(x) ? V - 1 : 0;
@@ -215,7 +223,7 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_held(NormArgs a, int6
     Weight<V> wt[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        pc[i] = piece_of<V>(i * threads + (int)threadIdx.x, (int)a.width, shift);
+        pc[i] = piece_of<V>(i * threads + me, (int)a.width, shift);
         s[i] = ld_vec<NT, u32x4>(x + pc[i].at * size);
         if (RES) q[i] = ld_vec<NT, u32x4>(res + pc[i].at * size);
     }
@@ -246,8 +254,8 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_held(NormArgs a, int6
         }
         ss += t;
     }
-    ss = team_all<OpSum>(ss, lds, &turn, waves);
-    // Stores only past the barrier: the sum or y may lie where x or the residual
+    ss = team(OpSum(), ss);
+    // Stores only past the exchange: the sum or y may lie where x or the residual
     // did, and the row's last vector shares elements with one of another wave.
     if (sum) {
 #pragma unroll
@@ -270,9 +278,9 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_held(NormArgs a, int6
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) most = OpMaxAbs::of(most, fabsf(y[i][e]));
-        most = team_all<OpMaxAbs>(most, lds, &turn, waves);
+        most = team(OpMaxAbs(), most);
         const Quant qt = quant_of<YT>(most);
-        if (threadIdx.x == 0) st_elem<float>(a.scale.p[r], row, qt.scale);
+        if (me == 0) st_elem<float>(a.scale.p[r], row, qt.scale);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (!owned<V>(pc[i])) continue;
@@ -298,6 +306,7 @@ struct NormGradArgs {
     int64_t width, part_width;   // part_width: room for the width in vectors
     int odd_stride;     // bf16 rows an odd number of elements apart
     int wdt;
+    int lanes;          // as NormArgs
     float eps, inv_width;
 };
 
@@ -343,15 +352,19 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_rows(NormGradArgs a)
 // row's sums are exchanged (PF; without it where the registers would not hold
 // two rows).  Each thread keeps the weight gradient of its own vectors in
 // registers over all the rows of its block; they are written in the vectors'
-// order (norm_grad_weight finds a column's place).
-template <int DT, int YT, int NV, bool PF, bool NT>
-__global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArgs a)
+// order (norm_grad_weight finds a column's place).  With narrow rows (NVS = 0) the
+// groups of a block take its rows in turn and join their weight gradients at
+// the end.
+template <int DT, int YT, int NVS, bool PF, bool NT>
+__global__ void __launch_bounds__(NVS ? kMostWaves * kWave : kNormThreads) norm_grad_held(NormGradArgs a)
 {
-    constexpr int V = kVec<DT>, size = kSize<DT>, ysize = kSize<YT>;
+    constexpr int V = kVec<DT>, size = kSize<DT>, ysize = kSize<YT>, NV = NVS ? NVS : 1;
     using Dy = Raw<V, YT>;
-    __shared__ float lds[4 * kMostWaves];
+    __shared__ float lds[NVS ? 4 * kMostWaves : kNormThreads * V];
     int turn = 0;
-    const int r = blockIdx.y, threads = blockDim.x, waves = threads / kWave;
+    const int r = blockIdx.y, threads = NVS ? blockDim.x : a.lanes, waves = threads / kWave;
+    const int me = NVS ? (int)threadIdx.x : (int)threadIdx.x & (threads - 1);
+    const int groups = NVS ? 1 : kNormThreads / threads, group = NVS ? 0 : (int)threadIdx.x / threads;
     const int64_t rows = a.rows[r];
     const bool has_q = a.dsum.p[r] != nullptr;
     Piece pc[NV];
@@ -368,7 +381,7 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArg
     const int64_t blocks = a.odd_stride ? ((int64_t)gridDim.x + 1 - kind) / 2 : gridDim.x;   // blocks
     const int64_t per = (mine + blocks - 1) / blocks, nth = blockIdx.x / step;
     const int64_t end = min(mine, (nth + 1) * per);
-    int64_t at_row = nth * per;
+    int64_t at_row = nth * per + group;
     const int shift = odd_start<DT>(a.s.p[r] + kind * a.s.pitch) ? V - 1 : 0;
     auto fetch = [&](int64_t k) {
         const int64_t at_row = k * step + kind;
@@ -383,7 +396,7 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArg
     };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        pc[i] = piece_of<V>(i * threads + (int)threadIdx.x, (int)a.width, shift);
+        pc[i] = piece_of<V>(i * threads + me, (int)a.width, shift);
         wt[i].load(a.weight, a.wdt, pc[i].at);
         q[i] = u32x4{0, 0, 0, 0};
     }
@@ -394,7 +407,7 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArg
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[i][e] = 0.0f;
     }
-    for (; at_row < end; ++at_row) {
+    for (; at_row < end; at_row += groups) {
         const int64_t row = at_row * step + kind;
         if (!PF) fetch(at_row);
         u32x4 s0[NV], q0[NV];
@@ -425,10 +438,10 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArg
             ss += t;
             gs += u;
         }
-        if (PF && at_row + 1 < end) fetch(at_row + 1);
-        ss = wave_all<OpSum>(ss);
-        gs = wave_all<OpSum>(gs);
-        if (waves > 1) {
+        if (PF && at_row + groups < end) fetch(at_row + groups);
+        ss = NVS ? wave_all<OpSum>(ss) : group_all<OpSum>(ss, threads);
+        gs = NVS ? wave_all<OpSum>(gs) : group_all<OpSum>(gs, threads);
+        if (NVS && waves > 1) {
             float *slot = lds + turn * 2 * kMostWaves;
             turn ^= 1;
             if (threadIdx.x % kWave == 0) {
@@ -457,11 +470,20 @@ __global__ void __launch_bounds__(kMostWaves * kWave) norm_grad_held(NormGradArg
         }
     }
     if (!a.part) return;
+    if (!NVS) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) lds[e * kNormThreads + (int)threadIdx.x] = acc[0][e];
+        __syncthreads();
+        if (group) return;
+        for (int g = 1; g < groups; ++g)
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[0][e] += lds[e * kNormThreads + g * threads + me];
+    }
     char *part = reinterpret_cast<char *>(a.part + ((int64_t)r * gridDim.x + blockIdx.x) * a.part_width);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (owned<V>(pc[i]))
-            st_values<V, kF32, false>(part + (int64_t)(i * threads + (int)threadIdx.x) * V * 4, acc[i]);
+            st_values<V, kF32, false>(part + (int64_t)(i * threads + me) * V * 4, acc[i]);
 }
 
 // The weight gradients: a block sums 64 columns of one rank's partial sums,
@@ -528,25 +550,42 @@ bool eight(int dt) { return dt == DDP_I8 || dt == DDP_E4M3; }
 bool eps_ok(float eps) { return eps >= 0.0f && std::isfinite(eps); }
 
 // The kernel for rows of `width` elements (and their shift), `vec` to a 16-byte
-// vector: the vectors each thread of a block holds, as few as let a block of at most 16
+// vector: a group of lanes to a row of at most `narrow` vectors, otherwise the vectors
+// each thread of a block holds, as few as let a block of at most 16
 // waves hold the row (more, smaller shares per thread measured as fast or
-// faster: 8 x 2048 x 4096 bf16 forward 87.0 us with 1, 87.2 us with 2), or 0
+// faster: 8 x 2048 x 4096 bf16 forward 87.0 us with 1, 87.2 us with 2), or none
 // where no block can and the row is read from memory in every pass.
+//
+// Narrow rows, 4 ranks, 268 MB in the forward and 403 in the backward, against a
+// wave to a row: bf16 width 64 forward 46 us and 224, backward 82 and 443; width 128
+// 43 and 115, 82 and 244; f32 width 128 48 and 68, 83 and 133.  From 33 vectors on
+// a wave to a row fills its lanes as well: forward bf16 512 43 and 42, f32 256 48
+// and 45.  The backward gains there from fewer blocks' partial sums: bf16 384 87 and
+// 110, 512 84 and 86.
+constexpr int64_t kNarrow = 32, kGradNarrow = 64;
 constexpr int64_t kMostThreads = kMostWaves * kWave;
-int held_vectors(int64_t width, int64_t vec, int most)
+struct Team {
+    int nv;        // vectors to a thread of norm_held or norm_grad_held, 0 for the other kernels
+    int lanes;     // to a row, 0: a block to a row
+    int threads;   // of a block
+    bool held() const { return nv || lanes; }
+};
+Team team_of(int64_t width, int64_t vec, int most, int64_t narrow)
 {
     const int64_t vecs = (width + vec - 1) / vec;
-    if (width < 2 * vec || vecs > most * kMostThreads) return 0;
-    return vecs <= kMostThreads ? 1 : vecs <= 2 * kMostThreads ? 2 : 4;
-}
-int held_threads(int64_t width, int64_t vec, int nv)
-{
-    return (int)(((width + vec - 1) / vec + nv * kWave - 1) / (nv * kWave)) * kWave;
+    if (width < 2 * vec || vecs > most * kMostThreads) return {0, 0, kNormThreads};
+    if (vecs <= narrow) {
+        int lanes = 2;
+        while (lanes < vecs) lanes *= 2;
+        return {0, lanes, kNormThreads};
+    }
+    const int nv = vecs <= kMostThreads ? 1 : vecs <= 2 * kMostThreads ? 2 : 4;
+    return {nv, 0, (int)((vecs + nv * kWave - 1) / (nv * kWave)) * kWave};
 }
 // What the backward holds per thread: four vectors only where they are f32 (a
 // thread's weights and weight gradient take two registers an element: with
 // bf16's eight to a vector the row would spill).
-int grad_held_vectors(int64_t width, int64_t vec) { return held_vectors(width, vec, vec == 4 ? 4 : 2); }
+Team grad_team(int64_t width, int64_t vec) { return team_of(width, vec, vec == 4 ? 4 : 2, kGradNarrow); }
 
 // Blocks of each rank in the backward, each with its own partial weight
 // gradient: eight waves, and one block at least, to each of the 256 CUs.  Two
@@ -554,34 +593,41 @@ int grad_held_vectors(int64_t width, int64_t vec) { return held_vectors(width, v
 // more waves bring no bandwidth and cost partial sums: 8 x 2048 x 4096 bf16
 // takes 97 us with 2048 waves in all, 136 with 1024, 103 with 4096 and 113
 // with 8192; 4096 x 8192 f32 (16 waves to a block) 102 us with 256 blocks and
-// 111 with 128.
-constexpr int64_t kCus = 256, kWavesPerCu = 8;
+// 111 with 128.  Narrow rows, whose last lanes may idle, take twelve: 4 x 87381 x 192
+// bf16 87 us, 103 with eight, 100 with 24.
+constexpr int64_t kCus = 256, kWavesPerCu = 8, kNarrowWavesPerCu = 12;
 int64_t grad_blocks(int64_t most, int32_t n_ranks, int64_t width, int64_t vec)
 {
-    const int nv = grad_held_vectors(width, vec);
-    const int64_t waves = nv ? held_threads(width, vec, nv) / kWave : kNormThreads / kWave;
-    int64_t blocks = kCus * std::max<int64_t>(1, kWavesPerCu / waves);
+    const Team t = grad_team(width, vec);
+    int64_t blocks = kCus * std::max<int64_t>(1, (t.lanes ? kNarrowWavesPerCu : kWavesPerCu) * kWave / t.threads);
+    if (t.lanes) {
+        const int64_t rows = kNormThreads / t.lanes;   // to a block at a time
+        most = std::max((most + rows - 1) / rows, std::min<int64_t>(most, 2));   // two, for odd_stride
+    }
     // rows too wide for registers: at most 64 MB of partial sums
-    if (!nv) blocks = std::min(blocks, std::max<int64_t>(8, ((int64_t)16 << 20) / width));
+    if (!t.held()) blocks = std::min(blocks, std::max<int64_t>(8, ((int64_t)16 << 20) / width));
     return std::max<int64_t>(1, std::min(most, blocks / n_ranks));
 }
 
 template <int DT, int YT, bool RES, bool NT>
-ddp_status_t launch_norm_as(const NormArgs &a, int shift, int64_t most, int32_t n_ranks, hipStream_t st)
+ddp_status_t launch_norm_as(NormArgs a, int shift, int64_t most, int32_t n_ranks, hipStream_t st)
 {
-    constexpr int V = kVec<DT>;
-    const int nv = held_vectors(a.width + shift, V, 4);
-    if (!nv) {
+    const Team t = team_of(a.width + shift, kVec<DT>, 4, kNarrow);
+    if (!t.held()) {
         const dim3 g((unsigned)std::min(most, kMostGridRows), (unsigned)n_ranks);
         norm_rows<DT, YT, RES><<<g, kNormThreads, 0, st>>>(a);
         return launched("norm kernel launch");
     }
-    const int threads = held_threads(a.width + shift, V, nv);
-    return launch_split(most, threads, "norm kernel launch", [&](int64_t b0, unsigned nb) {
+    a.lanes = t.lanes;
+    const int threads = t.lanes ? kWave : t.threads;
+    const int64_t rows = t.lanes ? kWave / t.lanes : 1;   // to a block
+    return launch_split((most + rows - 1) / rows, threads, "norm kernel launch", [&](int64_t b0, unsigned nb) {
         const dim3 g(nb, (unsigned)n_ranks);
-        if (nv == 1)
+        if (t.lanes)
+            norm_held<DT, YT, RES, 0, NT><<<g, threads, 0, st>>>(a, b0);
+        else if (t.nv == 1)
             norm_held<DT, YT, RES, 1, NT><<<g, threads, 0, st>>>(a, b0);
-        else if (nv == 2)
+        else if (t.nv == 2)
             norm_held<DT, YT, RES, 2, NT><<<g, threads, 0, st>>>(a, b0);
         else
             norm_held<DT, YT, RES, 4, NT><<<g, threads, 0, st>>>(a, b0);
@@ -589,19 +635,20 @@ ddp_status_t launch_norm_as(const NormArgs &a, int shift, int64_t most, int32_t 
 }
 
 template <int DT, int YT, bool NT>
-void launch_grad_as(const NormGradArgs &a, int shift, dim3 g, hipStream_t st)
+void launch_grad_as(NormGradArgs a, int shift, dim3 g, hipStream_t st)
 {
-    constexpr int V = kVec<DT>;
-    const int nv = grad_held_vectors(a.width + shift, V);
-    const int threads = nv ? held_threads(a.width + shift, V, nv) : kNormThreads;
-    if (nv == 1)
-        norm_grad_held<DT, YT, 1, true, NT><<<g, threads, 0, st>>>(a);
-    else if (nv == 2)
-        norm_grad_held<DT, YT, 2, true, NT><<<g, threads, 0, st>>>(a);
-    else if (nv == 4) {
-        if constexpr (DT == kF32) norm_grad_held<DT, YT, 4, false, NT><<<g, threads, 0, st>>>(a);
+    const Team t = grad_team(a.width + shift, kVec<DT>);
+    a.lanes = t.lanes;
+    if (t.lanes)
+        norm_grad_held<DT, YT, 0, true, NT><<<g, t.threads, 0, st>>>(a);
+    else if (t.nv == 1)
+        norm_grad_held<DT, YT, 1, true, NT><<<g, t.threads, 0, st>>>(a);
+    else if (t.nv == 2)
+        norm_grad_held<DT, YT, 2, true, NT><<<g, t.threads, 0, st>>>(a);
+    else if (t.nv == 4) {
+        if constexpr (DT == kF32) norm_grad_held<DT, YT, 4, false, NT><<<g, t.threads, 0, st>>>(a);
     } else
-        norm_grad_rows<DT, YT><<<g, threads, 0, st>>>(a);
+        norm_grad_rows<DT, YT><<<g, t.threads, 0, st>>>(a);
 }
 
 // Bytes moved from which a call's accesses are non-temporal: what no longer
@@ -780,7 +827,7 @@ ddp_status_t ddp_rms_norm_grad(const int64_t *rows, int32_t n_ranks, int64_t wid
         w.width = width;
         w.part_width = part_width;
         if (total > 0) set_rows(&w.s, s, r0, nr, esz);
-        w.vec = grad_held_vectors(width + shift, vec) ? (int)vec : 0;
+        w.vec = grad_team(width + shift, vec).held() ? (int)vec : 0;
         w.odd_stride = odd_stride;
         w.parts = (int32_t)blocks;
         w.part = static_cast<const float *>(workspace) + r0 * blocks * part_width;

@@ -91,6 +91,27 @@ __device__ __forceinline__ float wave_all(float x)
     return Op::of(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// The same among each group of `lanes` lanes, a power of two from 2 on.
+template <class Op>
+__device__ __forceinline__ float group_all(float x, int lanes)
+{
+    x = Op::of(x, dpp<0xB1>(x));
+    if (lanes > 2) x = Op::of(x, dpp<0x4E>(x));
+    if (lanes > 4) x = Op::of(x, dpp<0x141>(x));
+    if (lanes > 8) x = Op::of(x, dpp<0x140>(x));
+    if (lanes > 16) {
+        const uint32_t u = __float_as_uint(x);
+        const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        x = Op::of(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    if (lanes > 32) {
+        const uint32_t u = __float_as_uint(x);
+        const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        x = Op::of(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    return x;
+}
+
 // Every thread of a block of `waves` waves gets the block's value.  `lds`
 // holds `waves` floats; the first barrier lets an earlier use of it end.
 template <class Op>

@@ -224,6 +224,42 @@ def test_unusual_values(ddp, width, out):
             assert (y[1].float() == 0).all()
 
 
+@pytest.mark.parametrize("width", [9, 16, 31, 33, 64, 120, 128, 129, 193, 256, 257, 505, 512])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_narrow_rows(ddp, width, dtype):
+    """Several rows to a wave: one row to many, on and off a 4-byte boundary, in place, and few of
+    them on one rank beside many on another."""
+    for k, rows in enumerate(([1, 2], [2], [3, 0, 1000], [7, 9000])):
+        pad, shift = [(0, 0), (1, 1), (3, 0), (0, 1)][k]
+        x = [matrix(_rand(k + r, n, width, dtype), pad, shift) for r, n in enumerate(rows)]
+        res = [matrix(_rand(k + r + 9, n, width, dtype), pad, shift) for r, n in enumerate(rows)]
+        dy = [matrix(_rand(k + r + 20, n, width, dtype), pad, shift) for r, n in enumerate(rows)]
+        w = _weight(k, width, dtype).cuda()
+        old = [a.clone() for a in x]
+        codes = [torch.empty(n, width, device="cuda", dtype=torch.int8) for n in rows]
+        scale = [torch.empty(n, device="cuda") for n in rows]
+        ddp.rms_norm(x, w, codes, residual=res, scale=scale, eps=EPS)
+        ddp.rms_norm(x, w, res, residual=res, sum_out=x, eps=EPS)   # both in place
+        fresh = [matrix(_rand(k + r + 9, n, width, dtype), pad, shift) for r, n in enumerate(rows)]
+        for r, n in enumerate(rows):
+            if not n:
+                continue
+            s = norm_sum(old[r], fresh[r])
+            assert torch.equal(x[r], s), (width, rows)
+            check_norm(res[r], s, w, EPS, what=(width, rows, r))
+            check_norm(codes[r], s, w, EPS, scale[r], (width, rows, r))
+        s = [a.clone() for a in x]
+        dw = [torch.full((width,), math.nan, device="cuda") for _ in rows]
+        d0 = [a.clone() for a in dy]
+        ddp.rms_norm_grad(x, w, dy, dy, dsum=x, dweight=dw, eps=EPS)
+        for r, n in enumerate(rows):
+            if n:
+                check_norm_grad(dy[r], dw[r], s[r], w, d0[r], s[r], EPS, what=(width, rows, r))
+            else:
+                assert (dw[r] == 0).all()
+        assert all(gaps_untouched(a) for a, n in zip(x + res + dy, rows * 3) if n)
+
+
 @pytest.mark.parametrize("width", [7, 48, 4096, 40009])
 def test_tiny_rows_without_eps(ddp, width):
     """Rows whose mean square lies below the least normal float, forward and backward."""

@@ -1114,24 +1114,30 @@ int far_threads(int64_t vecs, int most)
     return (int)std::max<int64_t>(kWave, std::min<int64_t>(most, (vecs + kWave - 1) / kWave * kWave));
 }
 
+// Vectors to a thread: as few as blocks of 256 threads take, then 8 bf16 vectors (64
+// registers in all) or 16 f32 ones, and 16 bf16 ones for the largest rows, which
+// leave a CU one block but are still read once: 4 x 512 x 128256 208 us
+// and 250 with distill_far, 2 x 300 x 131072 75 and 92.
 template <int DT, bool NT>
-ddp_status_t launch_grad(const DistillArgs &a, int64_t most, hipStream_t st)
+ddp_status_t launch_grad(const DistillArgs &a, int shift, int64_t most, hipStream_t st)
 {
     constexpr int V = kVec<DT>;
-    const int64_t vecs = (a.vocab + (DT == kBF16 ? V - 1 : 0) + V - 1) / V;   // of a row that starts off a dword
-    constexpr int kBig = DT == kF32 ? 16 : 8;   // 64 exponentials to a thread
-    const int nv = a.vocab < V || vecs > kBig * kMostThreads ? 0
-                   : vecs <= 2 * 256 ? 2 : vecs <= kBig / 2 * 256 ? kBig / 2 : kBig;
+    const int64_t vecs = (a.vocab + shift + V - 1) / V;
+    constexpr int kMid = DT == kF32 ? 8 : 4, kBig = 2 * kMid;
+    const int nv = a.vocab < V || vecs > 16 * kMostThreads ? 0
+                   : vecs <= 2 * 256 ? 2 : vecs <= kMid * 256 ? kMid : vecs <= kBig * kMostThreads ? kBig : 16;
     const int threads = nv ? (int)((vecs + nv * kWave - 1) / (nv * kWave)) * kWave : far_threads(vecs, kFarThreads);
     const unsigned lds = entry_bytes(a.top);
     return launch_split(most, threads, "distillation kernel launch", [&](int64_t b0, unsigned nb) {
         const dim3 g(nb, (unsigned)a.n_ranks);
         if (nv == 2)
             distill_held<DT, 2, NT><<<g, threads, lds, st>>>(a, b0);
-        else if (nv == kBig / 2)
-            distill_held<DT, kBig / 2, NT><<<g, threads, lds, st>>>(a, b0);
-        else if (nv == kBig)
-            distill_held<DT, kBig, NT><<<g, threads, lds, st>>>(a, b0);
+        else if (nv == kMid)
+            distill_held<DT, kMid, NT><<<g, threads, lds, st>>>(a, b0);
+        else if (nv == 8)
+            distill_held<DT, 8, NT><<<g, threads, lds, st>>>(a, b0);
+        else if (nv == 16)
+            distill_held<DT, 16, NT><<<g, threads, lds, st>>>(a, b0);
         else
             distill_far<DT><<<g, threads, lds, st>>>(a, b0);
     });
@@ -1149,9 +1155,9 @@ ddp_status_t launch_loss(const DistillArgs &a, int64_t most, hipStream_t st)
 }
 
 template <int DT>
-ddp_status_t launch_rows(const DistillArgs &a, int64_t most, bool grad, bool nt, hipStream_t st)
+ddp_status_t launch_rows(const DistillArgs &a, int shift, int64_t most, bool grad, bool nt, hipStream_t st)
 {
-    if (grad) return nt ? launch_grad<DT, true>(a, most, st) : launch_grad<DT, false>(a, most, st);
+    if (grad) return nt ? launch_grad<DT, true>(a, shift, most, st) : launch_grad<DT, false>(a, shift, most, st);
     return launch_loss<DT>(a, most, st);
 }
 
@@ -1293,10 +1299,12 @@ ddp_status_t run_distill(bool grad, const int64_t *rows, int32_t n_ranks, int64_
             if (st != DDP_OK) return st;
         }
         const bool nt = total * vocab * esz * 2 >= kStreamBytes;
+        // elements a row may need beyond its own for its vectors to start on a 4-byte boundary
+        const int shift = dtype == DDP_BF16 && odd_rows(logits, rows, n_ranks) ? kVec<kBF16> - 1 : 0;
         st = for_groups(n_ranks, [&](int32_t r0, int32_t nr) {
             const DistillArgs a = group(r0, nr);
-            if (dtype == DDP_F32) return launch_rows<kF32>(a, most, grad, nt, hs);
-            return launch_rows<kBF16>(a, most, grad, nt, hs);
+            if (dtype == DDP_F32) return launch_rows<kF32>(a, 0, most, grad, nt, hs);
+            return launch_rows<kBF16>(a, shift, most, grad, nt, hs);
         });
         if (st != DDP_OK) return st;
     }

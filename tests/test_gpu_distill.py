@@ -214,7 +214,8 @@ def test_unusual_logits(ddp, vocab, many, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,vocab", [([2], 1000), ([3, 2], 50257), ([200], 32000), ([2], 150001), ([300], 1000),
-                                        ([300], 2051), ([300, 9], 32000), ([280], 50257), ([270], 61441)])
+                                        ([300], 2051), ([300, 9], 32000), ([280], 50257), ([270], 61441),
+                                        ([260], 100003)])
 def test_in_place(ddp, dtype, rows, vocab):
     z, t, i = _case(5, rows, vocab, 16, dtype)
     for x in i:

@@ -11,8 +11,8 @@
 // backward reads all of s anyway and sums its squares beside w dy s.
 //
 // Measured (rocprofv3, MI355X): 8 ranks x 2048 x 4096 bf16, forward with a
-// residual 537 MB in 87 us = 6.2 TB/s, backward 537 MB in 92 us + 4.8 us for
-// the weight gradients' second launch = 5.5 TB/s.
+// residual 537 MB in 88 us = 6.1 TB/s, backward 537 MB in 94 us = 5.7 TB/s,
+// and 4.7 us for the weight gradients' second launch.
 //
 // Rounding: s is rounded to its dtype because the rounded sum is what the next
 // layers add to, and what the backward is given; y, dx and dw are rounded once

@@ -1,7 +1,8 @@
 """Python binding of libddp.so: bucketed gradient synchronisation on MI355X.
 
-Argument marshalling only -- every step runs in the HIP library through its
-C ABI (``include/ddp.h``).  PyTorch supplies device memory and streams:
+Argument marshalling only (that of the calls over rows of tokens in C++,
+``_rows``) -- every step runs in the HIP library through its C ABI
+(``include/ddp.h``).  PyTorch supplies device memory and streams:
 tensors are passed by ``data_ptr()``, streams by ``torch.cuda.Stream``
 handles.  Importing this module loads ``libddp.so`` and raises if it has not
 been built; there is no fallback implementation.
@@ -18,10 +19,14 @@ from __future__ import annotations
 
 import ctypes
 import os
-from array import array
 from typing import List, Optional, Sequence
 
 import torch
+
+try:
+    from . import _rows
+except ImportError as e:
+    raise ImportError("_rows.so is not built; run __graft_entry__.build()") from e
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libddp.so")
@@ -127,7 +132,7 @@ def _load():
                                ctypes.c_int, ctypes.c_float, vp, ctypes.c_int, vp, vp, vp,
                                ctypes.c_int, ctypes.c_int32, vp, ctypes.c_int64, vp],
                               ctypes.c_int),
-        "ddp_rms_norm_grad_workspace": ([c_i64p, ctypes.c_int32, ctypes.c_int64], ctypes.c_int64),
+        "ddp_rms_norm_grad_workspace": ([vp, ctypes.c_int32, ctypes.c_int64], ctypes.c_int64),
         "ddp_distill_loss": ([vp, ctypes.c_int32, ctypes.c_int64, vp, ctypes.c_int,
                               ctypes.c_int32, vp, ctypes.c_int, vp, ctypes.c_int32, vp,
                               ctypes.c_float, vp, vp, vp, ctypes.c_int64, vp], ctypes.c_int),
@@ -135,7 +140,7 @@ def _load():
                               ctypes.c_int32, vp, ctypes.c_int, vp, ctypes.c_int32, vp,
                               ctypes.c_float, ctypes.c_float, vp, vp, vp, vp, ctypes.c_int64, vp],
                              ctypes.c_int),
-        "ddp_distill_workspace": ([c_i64p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32],
+        "ddp_distill_workspace": ([vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32],
                                   ctypes.c_int64),
         "ddp_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "ddp_abi_version": ([], ctypes.c_int32),
@@ -598,164 +603,30 @@ def accumulate(dst: Sequence, src: Sequence, length: Optional[int] = None, strea
 
 # ---------------------------------------------------------------- rows of tokens
 
-_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
-_NORM_OUT = {**_FLOATS, torch.int8: I8, torch.float8_e4m3fn: E4M3}
-_INDICES = {torch.int32: 4, torch.int64: 8}
-_ONE_F32 = {torch.float32: F32}
+_FLOATS = _rows.F32 | _rows.BF16
+_NORM_OUT = _FLOATS | _rows.I8 | _rows.E4M3
+_INDICES = _rows.I32 | _rows.I64   # their codes are their bytes
 
 
-class _Tokens:
-    """The operands of one call over every rank's rows of tokens, checked and
-    laid out as the C call takes them.  ``like[r]`` is rank r's matrix [..., width],
-    its rows one fixed distance apart; the other operands have its shape.
-
-    All pointer arrays and ddp_rows_t structures of a call go into one array of
-    64-bit words: an operand is known by its place there (``ref``) until ``done`` makes the
-    array.  (A call on small tensors is bound by this work: 5 us of about 10.)"""
-
-    __slots__ = ("device", "n", "rows", "width", "words", "fix")
-
-    def __init__(self, like: Sequence):
-        self.device = torch._C._cuda_getDevice()
-        self.n = len(like)
-        if self.n == 0:
-            raise ValueError("no ranks")
-        rows = []
-        width = 0
-        for t in like:
-            shape = t.shape
-            if len(shape) == 2:
-                n, w = shape
-            elif shape:
-                w = shape[-1]
-                n = t.numel() // max(w, 1)
-            else:
-                raise ValueError("a rank's tensor needs a dimension for the width")
-            width = width or w
-            rows.append(n)
-        if width < 1:
-            raise ValueError("the width is 0")
-        self.rows = rows
-        self.width = width
-        self.words = rows.copy()
-        self.fix = []          # (word, the word whose address it holds)
-
-    def _on_device(self, t):
-        if t.get_device() != self.device:
-            raise ValueError("tensor is not on the current GPU" if t.is_cuda else "tensor is not on a GPU")
-
-    def matrix(self, ts, what: str, codes, width: int):
-        """(dtype, ref of its ddp_rows_t) of one operand; (None, None) where it is absent."""
-        if ts is None:
-            return None, None
-        if len(ts) != self.n:
-            raise ValueError(f"{what}: one tensor per rank is required")
-        dtype, device, words = ts[0].dtype, self.device, self.words
-        if dtype not in codes:
-            raise TypeError(f"{what}: unsupported dtype {dtype}")
-        first = len(words)
-        stride = None
-        for t, n in zip(ts, self.rows):
-            if t.get_device() != device:
-                self._on_device(t)
-            if t.dtype != dtype:
-                raise ValueError(f"{what}: the ranks differ in dtype")
-            if t.dim() == 2:
-                pitch, step = t.stride()
-                if t.shape != (n, width):
-                    raise ValueError(f"{what}: {n} rows of {width} elements are required, got {tuple(t.shape)}")
-            else:
-                pitch, step = self._flat_stride(t, n, width, what)
-            if n > 0:
-                if step != 1 and width > 1:
-                    raise ValueError(f"{what}: the elements of a row are not consecutive")
-                if n > 1 and pitch != stride:
-                    if stride is not None:
-                        raise ValueError(f"{what}: the ranks differ in row stride")
-                    stride = pitch
-            words.append(t.data_ptr())
-        at = len(words)
-        self.fix.append((at, first))
-        words.append(0)
-        words.append(width if stride is None else stride)
-        return dtype, at
-
-    @staticmethod
-    def _flat_stride(t, n, width, what):
-        """Strides of a tensor of other than two dimensions as a matrix."""
-        shape = t.shape
-        if not shape or shape[-1] != width or t.numel() != n * width:
-            raise ValueError(f"{what}: {n} rows of {width} elements are required, got {tuple(shape)}")
-        try:
-            return t.view(-1, width).stride()
-        except RuntimeError:
-            raise ValueError(f"{what}: the rows are not one fixed distance apart") from None
-
-    def vectors(self, ts, what: str, length=None, codes=_ONE_F32):
-        """(dtype, ref of the pointer array) of one vector per rank: ``length`` elements, or one
-        for each of the rank's rows."""
-        if ts is None:
-            return None, None
-        if len(ts) != self.n:
-            raise ValueError(f"{what}: one tensor per rank is required")
-        dtype, first = ts[0].dtype, len(self.words)
-        if dtype not in codes:
-            raise TypeError(f"{what}: unsupported dtype {dtype}")
-        for t, n in zip(ts, self.rows):
-            self._on_device(t)
-            if t.dtype != dtype:
-                raise ValueError(f"{what}: the ranks differ in dtype")
-            want = n if length is None else length
-            if t.numel() != want:
-                raise ValueError(f"{what}: {want} elements are required, got {t.numel()}")
-            if not t.is_contiguous():
-                raise ValueError(f"{what}: tensor is not contiguous")
-            self.words.append(t.data_ptr())
-        return dtype, first
-
-    def shared(self, t, what: str, length: int, codes):
-        """(dtype code, address) of a tensor every rank shares; (F32, None) where it is absent."""
-        if t is None:
-            return F32, None
-        self._on_device(t)
-        if t.dtype not in codes:
-            raise TypeError(f"{what}: unsupported dtype {t.dtype}")
-        if t.numel() != length:
-            raise ValueError(f"{what}: {length} elements are required, got {t.numel()}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: tensor is not contiguous")
-        return codes[t.dtype], t.data_ptr()
-
-    def workspace(self, t, need, stream, *more):
-        """(address, bytes, tensor) of the caller's workspace, or of a new one of need(rows, n,
-        width, *more) bytes that belongs to the call's stream."""
-        if t is None:
-            nbytes = _workspace_bytes(need, self.rows, self.width, *more)
-            if stream is None:
-                t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-            else:
-                s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-                with torch.cuda.stream(s):
-                    t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-            return t.data_ptr(), nbytes, t
-        self._on_device(t)
-        if not t.is_contiguous():
-            raise ValueError("workspace: tensor is not contiguous")
-        return t.data_ptr(), t.numel() * t.element_size(), t
-
-    def stream(self, stream) -> int:
+def _workspace(t, device: int, need, rows, n: int, width: int, stream, *more):
+    """(address, bytes, tensor) of the caller's workspace, or of a new one of need(rows, n,
+    width, *more) bytes that belongs to the call's stream."""
+    if t is None:
+        nbytes = need(rows, n, width, *more)
+        if nbytes < 0:
+            raise DDPError(1, need.__name__)
         if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.device)
-        return _stream_handle(stream)
+            t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        else:
+            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+            with torch.cuda.stream(s):
+                t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    _, at, nbytes = _rows.span(device, t, "workspace", 0, -1)
+    return at, nbytes, t
 
-    def done(self, *refs):
-        """The array (to be kept until the call returns) and the address of each ref, None for
-        None; ref 0 is the row counts."""
-        words = array("q", self.words)
-        base = words.buffer_info()[0]
-        for at, first in self.fix:
-            words[at] = base + 8 * first
-        return words, [None if r is None else base + 8 * r for r in refs]
+
+def _stream_of(stream, device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream_handle(stream)
 
 
 def rms_norm(x: Sequence, weight, out: Sequence, residual: Optional[Sequence] = None,
@@ -764,19 +635,17 @@ def rms_norm(x: Sequence, weight, out: Sequence, residual: Optional[Sequence] = 
     """out[r] = s * weight / sqrt(mean(s^2) + eps) over the last dimension, s = x[r] +
     residual[r], for every rank in one launch (``ddp_rms_norm``).  ``sum_out``
     receives s; an int8 or float8_e4m3fn ``out`` comes with ``scale``, one f32 per row."""
-    tk = _Tokens(x)
-    width = tk.width
-    dt, xr = tk.matrix(x, "x", _FLOATS, width)
-    ydt, yr = tk.matrix(out, "out", _NORM_OUT, width)
-    rdt, rr = tk.matrix(residual, "residual", _FLOATS, width)
-    sdt, sr = tk.matrix(sum_out, "sum_out", _FLOATS, width)
-    if (rdt or dt) != dt or (sdt or dt) != dt:
+    device = torch._C._cuda_getDevice()
+    words, n, width, _, rows, dt, xr, ydt, yr, rdt, rr, sdt, sr, _, sc = _rows.pack(
+        device, (x, "x", _FLOATS, _rows.LIKE), (out, "out", _NORM_OUT, _rows.LIKE),
+        (residual, "residual", _FLOATS, _rows.LIKE), (sum_out, "sum_out", _FLOATS, _rows.LIKE),
+        (scale, "scale", _rows.F32, _rows.ROWS))
+    if yr is None:
+        raise ValueError("out is required")
+    if (rdt is not None and rdt != dt) or (sdt is not None and sdt != dt):
         raise ValueError("residual and sum_out must have x's dtype")
-    _, sc = tk.vectors(scale, "scale")
-    wdt, wp = tk.shared(weight, "weight", width, _FLOATS)
-    words, (rows, xr, rr, sr, yr, sc) = tk.done(0, xr, rr, sr, yr, sc)
-    st = lib.ddp_rms_norm(rows, tk.n, width, xr, rr, _FLOATS[dt], wp, wdt, eps, sr, yr, _NORM_OUT[ydt], sc,
-                          tk.stream(stream))
+    wdt, wp, _ = _rows.span(device, weight, "weight", _FLOATS, width)
+    st = lib.ddp_rms_norm(rows, n, width, xr, rr, dt, wp, wdt, eps, sr, yr, ydt, sc, _stream_of(stream, device))
     if st:
         _check(st, "ddp_rms_norm")
 
@@ -800,23 +669,22 @@ def rms_norm_grad(s: Sequence, weight, dy: Sequence, dx: Sequence, dsum: Optiona
     """The backward of ``rms_norm`` (``ddp_rms_norm_grad``): dx[r] the gradient of
     s[r] (so of x and the residual), dweight[r] the rank's weight gradient, stored or, with
     ``accumulate``, added to what is there."""
-    tk = _Tokens(s)
-    width = tk.width
-    dt, sr = tk.matrix(s, "s", _FLOATS, width)
-    ydt, yr = tk.matrix(dy, "dy", _FLOATS, width)
-    ddt, dr = tk.matrix(dsum, "dsum", _FLOATS, width)
-    xdt, xr = tk.matrix(dx, "dx", _FLOATS, width)
-    if xdt != dt or (ddt or dt) != dt:
+    device = torch._C._cuda_getDevice()
+    words, n, width, _, rows, dt, sr, ydt, yr, ddt, dr, xdt, xr, gdt, wg = _rows.pack(
+        device, (s, "s", _FLOATS, _rows.LIKE), (dy, "dy", _FLOATS, _rows.LIKE),
+        (dsum, "dsum", _FLOATS, _rows.LIKE), (dx, "dx", _FLOATS, _rows.LIKE),
+        (dweight, "dweight", _FLOATS, _rows.WIDTH))
+    if yr is None or xr is None:
+        raise ValueError("dy and dx are required")
+    if xdt != dt or (ddt is not None and ddt != dt):
         raise ValueError("dx and dsum must have s's dtype")
-    wdt, wp = tk.shared(weight, "weight", width, _FLOATS)
-    gdt, wg = tk.vectors(dweight, "dweight", width, _FLOATS)
+    wdt, wp, _ = _rows.span(device, weight, "weight", _FLOATS, width)
     ws, nbytes, keep = None, 0, None
     if dweight is not None:
-        ws, nbytes, keep = tk.workspace(workspace, lib.ddp_rms_norm_grad_workspace, stream)
-    words, (rows, sr, yr, dr, xr, wg) = tk.done(0, sr, yr, dr, xr, wg)
-    st = lib.ddp_rms_norm_grad(rows, tk.n, width, sr, _FLOATS[dt], wp, wdt, eps, yr, _FLOATS[ydt], dr, xr, wg,
-                               F32 if gdt is None else _FLOATS[gdt], 1 if accumulate else 0, ws, nbytes,
-                               tk.stream(stream))
+        ws, nbytes, keep = _workspace(workspace, device, lib.ddp_rms_norm_grad_workspace, rows, n, width, stream)
+    st = lib.ddp_rms_norm_grad(rows, n, width, sr, dt, wp, wdt, eps, yr, ydt, dr, xr, wg,
+                               F32 if gdt is None else gdt, 1 if accumulate else 0, ws, nbytes,
+                               _stream_of(stream, device))
     if st:
         _check(st, "ddp_rms_norm_grad")
 
@@ -829,29 +697,23 @@ def distill_workspace(rows: Sequence[int], vocab: int, top: int) -> int:
 
 def _distill(logits, teacher, index, dlogits, loss, row_loss, token_weight, temperature, grad_scale,
              workspace, stream):
-    tk = _Tokens(logits)
-    vocab = tk.width
-    dt, zr = tk.matrix(logits, "logits", _FLOATS, vocab)
-    if len(teacher) != tk.n or teacher[0].dim() == 0:
-        raise ValueError("teacher: one tensor per rank is required")
-    top = teacher[0].shape[-1]
-    tdt, tr = tk.matrix(teacher, "teacher", _FLOATS, top)
-    idt, ir = tk.matrix(index, "index", _INDICES, top)
-    _, tw = tk.vectors(token_weight, "token_weight")
-    _, rl = tk.vectors(row_loss, "row_loss")
-    _, lp = tk.shared(loss, "loss", 1, _ONE_F32)
-    gdt, gr = tk.matrix(dlogits, "dlogits", _FLOATS, vocab)
-    if (gdt or dt) != dt:
+    device = torch._C._cuda_getDevice()
+    words, n, vocab, top, rows, dt, zr, tdt, tr, idt, ir, _, tw, _, rl, gdt, gr = _rows.pack(
+        device, (logits, "logits", _FLOATS, _rows.LIKE), (teacher, "teacher", _FLOATS, _rows.OWN),
+        (index, "index", _INDICES, _rows.OWN), (token_weight, "token_weight", _rows.F32, _rows.ROWS),
+        (row_loss, "row_loss", _rows.F32, _rows.ROWS), (dlogits, "dlogits", _FLOATS, _rows.LIKE))
+    if tr is None or ir is None:
+        raise ValueError("teacher and index are required")
+    if gdt is not None and gdt != dt:
         raise ValueError("dlogits must have the logits' dtype")
-    ws, nbytes, keep = tk.workspace(workspace, lib.ddp_distill_workspace, stream, top)
-    words, (rows, zr, tr, ir, tw, rl, gr) = tk.done(0, zr, tr, ir, tw, rl, gr)
+    _, lp, _ = _rows.span(device, loss, "loss", _rows.F32, 1)
+    ws, nbytes, keep = _workspace(workspace, device, lib.ddp_distill_workspace, rows, n, vocab, stream, top)
     if dlogits is None:
-        st = lib.ddp_distill_loss(rows, tk.n, vocab, zr, _FLOATS[dt], top, tr, _FLOATS[tdt], ir,
-                                  _INDICES[idt], tw, temperature, lp, rl, ws, nbytes, tk.stream(stream))
+        st = lib.ddp_distill_loss(rows, n, vocab, zr, dt, top, tr, tdt, ir, idt, tw, temperature, lp, rl, ws, nbytes,
+                                  _stream_of(stream, device))
     else:
-        st = lib.ddp_distill_grad(rows, tk.n, vocab, zr, _FLOATS[dt], top, tr, _FLOATS[tdt], ir,
-                                  _INDICES[idt], tw, temperature, grad_scale, gr, lp, rl, ws, nbytes,
-                                  tk.stream(stream))
+        st = lib.ddp_distill_grad(rows, n, vocab, zr, dt, top, tr, tdt, ir, idt, tw, temperature, grad_scale, gr, lp,
+                                  rl, ws, nbytes, _stream_of(stream, device))
     if st:
         _check(st, "ddp_distill_loss" if dlogits is None else "ddp_distill_grad")
 

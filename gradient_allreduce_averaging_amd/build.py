@@ -1,4 +1,4 @@
-"""Build libddp.so (HIP, gfx950) in-tree with hipcc.
+"""Build libddp.so (HIP, gfx950) in-tree with hipcc, and _rows.so with g++.
 
 Flags: IEEE FP32 throughout (no FMA contraction, denormals kept, no fast
 math) so every add and multiply is one correctly rounded binary32 operation;
@@ -29,6 +29,29 @@ PROBE_SRC = "probe.hip"
 PROBE_LIB = os.path.join(HERE, "libddp_probe.so")
 
 
+ROWS_SRC = "rows_py.cpp"
+ROWS_LIB = os.path.join(HERE, "_rows.so")
+
+
+def _build_rows(verbose: bool) -> str:
+    """The Python module that lays out the tensors of calls over rows of tokens (host code
+    against torch's headers)."""
+    import importlib.util
+    import sysconfig
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    include = os.path.join(torch_dir, "include")
+    tmp = ROWS_LIB + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, ROWS_SRC),
+           "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, ROWS_LIB)
+    return ROWS_LIB
+
+
 def _build_probe(verbose: bool) -> str:
     """The benchmark's access-pattern probe, a library of its own."""
     tmp = PROBE_LIB + ".tmp%d" % os.getpid()
@@ -56,11 +79,13 @@ def _compile(src: str, verbose: bool) -> str:
 
 def build(verbose: bool = False) -> str:
     """Compile every source (in parallel, one hipcc per source) and link
-    libddp.so (and libddp_probe.so) next to this file."""
+    libddp.so (and libddp_probe.so and _rows.so) next to this file."""
     from concurrent.futures import ThreadPoolExecutor
-    jobs = max(1, min(len(SOURCES), len(os.sched_getaffinity(0)), 16))
+    jobs = max(1, min(len(SOURCES) + 1, len(os.sched_getaffinity(0)), 16))
     with ThreadPoolExecutor(jobs) as ex:
+        rows = ex.submit(_build_rows, verbose)
         objs = list(ex.map(lambda src: _compile(src, verbose), SOURCES))
+        rows.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp] + objs
     if verbose:

@@ -213,3 +213,34 @@ def test_workspace_sizes():
         ddp.distill_workspace([-1], 8, 1)
     with pytest.raises(ddp.DDPError):
         ddp.rms_norm_grad_workspace([1], 0)
+
+
+def test_marshalling_refuses_what_is_no_list_of_gpu_tensors():
+    import torch
+    R = ddp._rows
+    x = torch.zeros(2, 8)
+
+    def pack(ts, more=None):
+        rest = () if more is None else ((more, "y", R.F32, R.LIKE),)
+        return R.pack(0, (ts, "x", R.F32, R.LIKE), *rest)
+
+    for bad in (x.to_sparse(), x):
+        with pytest.raises(ValueError, match="x: tensor is not on a GPU"):
+            pack([bad])
+    with pytest.raises(ValueError, match="no ranks"):
+        pack([])
+    with pytest.raises(ValueError, match="y: one tensor per rank"):
+        pack([x, x], [x])
+    for bad in ([1.0], [None], None, 3):
+        with pytest.raises(TypeError):
+            pack(bad)
+    for bad in ((), (0,), (0, 1), (0, (1, 2)), ("x", ([x], "x", 1, -1))):
+        with pytest.raises(TypeError):
+            R.pack(*bad)
+    assert R.span(0, None, "w", R.F32, 8) == (0, None, 0)
+    with pytest.raises(ValueError, match="w: tensor is not on a GPU"):
+        R.span(0, x, "w", R.F32, 8)
+    with pytest.raises(TypeError):
+        R.span(0, 1.0, "w", R.F32, 8)
+    with pytest.raises(TypeError):
+        R.span(0, x)

@@ -186,16 +186,24 @@ __device__ __forceinline__ bool teacher_of(const DistillArgs &a, int r, int64_t 
         en.prob[l] = first.logit(a);
         en.z[l] = first.student<DT>();
     }
-#pragma unroll 1
-    for (int k0 = kWave; k0 < padded; k0 += kWave) {
-        const int k = k0 + l;
-        if (k >= padded) break;
-        float t = 0.0f;
-        const int32_t j = k < a.top ? entry_of(a, index, teacher, k, &t) : -1;
-        en.at[k] = j;
-        en.prob[k] = t;
-        if (j >= 0) tm = fmaxf(tm, t);
-        en.z[k] = j >= lo && j < hi ? load_elem<DT>(z, j) : 0.0f;
+    // four to a step, and no load behind a condition: past the last entry it is the last one's
+    for (int k0 = kWave; k0 < padded; k0 += 4 * kWave) {
+        int32_t j[4];
+        float t[4], zs[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) j[u] = entry_of(a, index, teacher, min(k0 + u * kWave + l, a.top - 1), &t[u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) zs[u] = load_elem<DT>(z, j[u] >= lo && j[u] < hi ? j[u] : lo);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = k0 + u * kWave + l;
+            if (k >= padded) break;
+            if (k >= a.top) j[u] = -1;
+            en.at[k] = j[u];
+            en.prob[k] = t[u];
+            en.z[k] = zs[u];
+            if (j[u] >= 0) tm = fmaxf(tm, t[u]);
+        }
     }
     tm = wave_all<OpMax>(tm);
     float mass = 0.0f;
@@ -299,10 +307,11 @@ __device__ __forceinline__ void note_row(const DistillArgs &a, int r, int64_t ro
 // and the others nothing, so every place is stored once.  Each block also sums
 // its tokens' weights into a part of D, which the first row's gradient needs.
 //
-// Indices that occur twice are found by a table of 32 bits to an entry, hashed by
-// the index: an entry that finds its bit set is suspect (one in 64 by chance, at
-// most), and only for suspects are all the entries compared.  What a group of
-// equal indices gets does not depend on which of them was suspected.
+// Indices that occur twice are found by a table of 32 bits to an entry, each
+// setting two of them, hashed by the index: an entry that finds both set is
+// suspect (one in several hundred by chance), and only for suspects are all the
+// entries compared.  What a group of equal indices gets does not depend on which of
+// them was suspected.
 constexpr int kTeacherWords = 3;   // LDS words to an entry: place, p, bits
 
 struct TokenEntries {
@@ -326,13 +335,22 @@ __device__ __forceinline__ bool teacher_token(const DistillArgs &a, int r, int64
     int32_t *at = te.at;
     float *prob = te.prob;
     float tm = -INFINITY;
-    for (int k = l; k < padded; k += kWave) {
-        float t = 0.0f;
-        const int32_t j = k < a.top ? entry_of(a, index, teacher, k, &t) : -1;
-        at[k] = j;
-        prob[k] = t;
-        te.bits[k] = 0;
-        if (j >= 0) tm = fmaxf(tm, t);
+    // four to a step, and no load behind a condition: past the last entry it is the last one's
+    for (int k0 = 0; k0 < padded; k0 += 4 * kWave) {
+        int32_t j[4];
+        float t[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) j[u] = entry_of(a, index, teacher, min(k0 + u * kWave + l, a.top - 1), &t[u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = k0 + u * kWave + l;
+            if (k >= padded) break;
+            if (k >= a.top) j[u] = -1;
+            at[k] = j[u];
+            prob[k] = t[u];
+            te.bits[k] = 0;
+            if (j[u] >= 0) tm = fmaxf(tm, t[u]);
+        }
     }
     tm = wave_all<OpMax>(tm);
     if (tm == -INFINITY) return false;
@@ -356,9 +374,13 @@ __device__ __forceinline__ bool teacher_token(const DistillArgs &a, int r, int64
         const int32_t mine = k0 + l < a.top ? at[k0 + l] : -1;
         bool suspect = false;
         if (mine >= 0) {
-            const uint32_t h = (uint32_t)mine * 0x9E3779B1u;
-            const uint32_t bit = 1u << (h >> 27);
-            suspect = atomicOr(&te.bits[((h & 0x7ffffffu) * (uint64_t)(uint32_t)padded) >> 27], bit) & bit;
+            // two places of the table by two hashes, the bit within each by their top 5 bits
+            auto mark = [&](uint32_t h) {
+                const uint32_t bit = 1u << (h >> 27);
+                return (atomicOr(&te.bits[((h & 0x7ffffffu) * (uint64_t)(uint32_t)padded) >> 27], bit) & bit) != 0;
+            };
+            const bool one = mark((uint32_t)mine * 0x9E3779B1u), two = mark((uint32_t)mine * 0x85EBCA6Bu + 0x3C6EF372u);
+            suspect = one && two;
         }
         uint64_t todo = __ballot(suspect);
         while (todo) {
